@@ -166,7 +166,7 @@ def _plain_loss(s):
     c = s["case"]
     E, k = c["E"], c["k"]
     l = s["logits"].float()
-    live = (l > -math.inf).any(1) if s["mask"] is None else (l > -math.inf).any(1) & s["mask"]
+    live = (l != -math.inf).any(1) if s["mask"] is None else (l != -math.inf).any(1) & s["mask"]
     n = live.sum().clamp(min=1)
     idx = s["idx"].long() if s["idx"] is not None else torch.sort(l, dim=1, descending=True, stable=True)[1][:, :k]
     hit = (idx.unsqueeze(2) == torch.arange(E, device=l.device)).sum(1)           # [T, E]
@@ -281,7 +281,7 @@ def _exact_loss(s):
     c = s["case"]
     l = s["logits"].double()
     T, E = l.shape
-    keep = torch.isfinite(l).any(1)
+    keep = ~torch.isneginf(l).all(1)
     if s["mask"] is not None:
         keep = keep & s["mask"]
     l, n = l[keep], max(1, int(keep.sum()))
