@@ -339,8 +339,58 @@ L4MOE_API const char *l4moe_kernel_name(int slot);
 /* Number of kernels this handle has launched so far. */
 L4MOE_API uint64_t l4moe_launch_count(const l4moe_handle *h);
 
+/* ------------------------------------------------------------------------
+ * Operators next to the layer.  They take no handle and keep nothing between
+ * calls: every buffer is the caller's, on the current device, and the call
+ * enqueues its kernels on `stream` without a host synchronisation or an
+ * allocation (they can be captured into a CUDA graph).  Calls may overlap on
+ * different streams as long as their outputs and workspaces differ.
+ * l4moe_last_error(NULL) has the message of this thread's last refused call. */
+
+typedef enum { L4MOE_ELEM_F32 = 0, L4MOE_ELEM_BF16 = 1, L4MOE_ELEM_F16 = 2 } l4moe_elem;
+
+/* How a logit becomes an expert's share of its token: softmax over the
+ * experts, or the sigmoid (the layer's gate) divided by the sum of the
+ * token's sigmoids. */
+typedef enum { L4MOE_SCORE_SOFTMAX = 0, L4MOE_SCORE_SIGMOID = 1 } l4moe_score;
+
+/* The losses that train a router, and the per-expert counts of its choices:
+ *   counts_e = entries that choose expert e, f_e = counts_e / (k n),
+ *   balance  = E sum_e f_e mean_t(share_te)   (1 for even use),
+ *   z        = mean_t(logsumexp(logits_t)^2),
+ *   loss     = balance_weight balance + z_weight z
+ * over the n counted rows: those that mask [T] keeps (bytes, 0 = left out;
+ * NULL = all) and that hold a logit other than -inf.  A NaN or +inf in a
+ * counted row makes balance, z and loss NaN; rows left out may hold anything.
+ * With no counted row all values are 0.  logits [T, E] of `type`, rows ld
+ * elements apart, 1 <= E <= 256, 1 <= k <= min(4, E).  idx NULL: each row
+ * chooses as the layer's router does (the k largest logits, the lower index
+ * first among equal ones, NaN only when no number is left); else idx [T, k]
+ * (int32, e.g. l4moe_get_routing's) holds the choices, and an entry outside
+ * [0, E) is a dropped one that counts for no expert.
+ * result (device): L4MOE_ROUTER_LOSS_WORDS(E) 4-byte words: loss, balance,
+ * z, n as fp32; counts [E] as int32; then what the gradient call needs.
+ * workspace (device): l4moe_router_loss_workspace(T, E) bytes, free to be
+ * used again once the call's work has run.  Sums are made in a fixed order:
+ * equal inputs give equal bits. */
+#define L4MOE_ROUTER_LOSS_WORDS(E) (4 + 2 * (E) + 1)
+L4MOE_API size_t l4moe_router_loss_workspace(int T, int E);
+L4MOE_API l4moe_status l4moe_router_loss(int T, int E, int k, const void *logits, l4moe_elem type, long long ld,
+                               const uint8_t *mask, const int32_t *idx, l4moe_score score,
+                               float balance_weight, float z_weight, float *result, void *workspace,
+                               size_t ws_bytes, void *stream);
+
+/* The gradient of that loss with respect to the logits, times *upstream (a
+ * device fp32, NULL = 1): dlogits [T, E] of the logits' type, rows ldd
+ * elements apart.  logits, type, ld, mask and score as in the call that
+ * filled result.  The counts have no derivative.  Rows left out get zeros.
+ * dlogits must not overlap the logits. */
+L4MOE_API l4moe_status l4moe_router_loss_grad(int T, int E, const void *logits, l4moe_elem type, long long ld,
+                                    const uint8_t *mask, l4moe_score score, const float *result,
+                                    const float *upstream, void *dlogits, long long ldd, void *stream);
+
 /* Message for the handle's last non-OK status ("" if none); h may be NULL
- * for errors of l4moe_create. */
+ * for errors of l4moe_create and of the operators without a handle. */
 L4MOE_API const char *l4moe_last_error(const l4moe_handle *h);
 
 /* Static name of a status code. */

@@ -6,6 +6,7 @@ if the compiled library is missing or the call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -22,7 +23,8 @@ EXPORTED = ("l4moe_create", "l4moe_destroy", "l4moe_workspace_size", "l4moe_set_
             "l4moe_launch_count", "l4moe_last_error", "l4moe_status_string", "l4moe_version",
             "l4moe_set_timing", "l4moe_read_timing", "l4moe_kernel_name",
             "l4moe_forward_static", "l4moe_join_host", "l4moe_set_top_k",
-            "l4moe_set_weight_scales", "l4moe_selftest_wait", "l4moe_set_act_fp8", "l4moe_get_plan")
+            "l4moe_set_weight_scales", "l4moe_selftest_wait", "l4moe_set_act_fp8", "l4moe_get_plan",
+            "l4moe_router_loss_workspace", "l4moe_router_loss", "l4moe_router_loss_grad")
 STATIC_WORKSPACE_BYTES = 32 << 20
 NUM_KERNELS = 6
 
@@ -88,6 +90,11 @@ def load_library():
     lib.l4moe_selftest_wait.argtypes = [vp, ctypes.c_double, vp]
     lib.l4moe_read_timing.argtypes = [vp, ctypes.POINTER(ctypes.c_double),
                                       ctypes.POINTER(ctypes.c_uint64)]
+    f32, i64 = ctypes.c_float, ctypes.c_longlong
+    lib.l4moe_router_loss_workspace.argtypes = [i32, i32]
+    lib.l4moe_router_loss_workspace.restype = sz
+    lib.l4moe_router_loss.argtypes = [i32, i32, i32, vp, i32, i64, vp, vp, i32, f32, f32, vp, vp, sz, vp]
+    lib.l4moe_router_loss_grad.argtypes = [i32, i32, vp, i32, i64, vp, i32, vp, vp, vp, i64, vp]
     lib.l4moe_kernel_name.argtypes = [i32]
     lib.l4moe_kernel_name.restype = ctypes.c_char_p
     for name in ("l4moe_create", "l4moe_set_workspace", "l4moe_set_router_bias",
@@ -95,7 +102,7 @@ def load_library():
                  "l4moe_get_routing", "l4moe_check_device_status", "l4moe_version",
                  "l4moe_set_timing", "l4moe_read_timing", "l4moe_forward_static",
                  "l4moe_join_host", "l4moe_set_top_k", "l4moe_set_weight_scales", "l4moe_selftest_wait",
-                 "l4moe_set_act_fp8", "l4moe_get_plan"):
+                 "l4moe_set_act_fp8", "l4moe_get_plan", "l4moe_router_loss", "l4moe_router_loss_grad"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -148,6 +155,38 @@ def _where(t, name, host=False):
     """Device check of one argument (after every shape and dtype check)."""
     if host == t.is_cuda:
         raise ValueError(f"l4moe: {name} must be a {'host' if host else 'CUDA'} tensor")
+
+
+# element types of the operators that take no handle (l4moe_elem)
+ELEMS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def check_op(st: int):
+    """Raise for a refused call of an operator that takes no handle."""
+    if st != OK:
+        raise L4MoEError(st, load_library().l4moe_last_error(None).decode())
+
+
+@contextlib.contextmanager
+def op_stream(tensor, stream):
+    """Run one operator on `tensor`'s device and on `stream` (a torch stream
+    or a raw handle; None: that device's current one): both are current
+    inside, so buffers allocated there belong to the stream that uses them.
+    Yields the raw handle."""
+    dev = tensor.device
+    if stream is None:
+        if dev.index == torch.cuda.current_device():
+            yield torch.cuda.current_stream(dev).cuda_stream
+        else:
+            with torch.cuda.device(dev):
+                yield torch.cuda.current_stream(dev).cuda_stream
+        return
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    if stream.device != dev:
+        raise ValueError(f"l4moe: stream of {stream.device}, tensors on {dev}")
+    with torch.cuda.stream(stream):
+        yield stream.cuda_stream
 
 
 class _DevView:

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -19,6 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libl4moe.so")
+OBJ = os.path.join(PKG, "build")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -45,19 +47,56 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _includes(path: str, seen=None) -> set:
+    """path and the package's own headers it includes, directly or not."""
+    seen = set() if seen is None else seen
+    if path in seen:
+        return seen
+    seen.add(path)
+    with open(path) as f:
+        for name in re.findall(r'^\s*#include\s+"([^"]+)"', f.read(), re.M):
+            for folder in (CSRC, INCLUDE):
+                if os.path.exists(os.path.join(folder, name)):
+                    _includes(os.path.join(folder, name), seen)
+    return seen
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile every source (side by side; one whose object is newer than all
+    it includes is kept) and link the library."""
     if not force and up_to_date():
         return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
-           "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared", "-cudart", "static",
-           "-I", INCLUDE, "-I", CSRC, "-o", tmp, *_sources()]
+    os.makedirs(OBJ, exist_ok=True)
+    flags = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
+             "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
+        flags.insert(0, "-Xptxas=-v")
+    jobs, objects = [], []
+    for src in _sources():
+        obj = os.path.join(OBJ, os.path.basename(src)[:-3] + ".o")
+        objects.append(obj)
+        if not force and os.path.exists(obj) and \
+                all(os.path.getmtime(p) <= os.path.getmtime(obj) for p in _includes(src)):
+            continue
+        tmp = f"{obj}.tmp{os.getpid()}.o"
+        cmd = [_nvcc(), *flags, "-c", src, "-o", tmp]
+        jobs.append((cmd, tmp, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    failed = None
+    for cmd, tmp, obj, p in jobs:
+        out = p.communicate()[0]
+        if verbose or p.returncode != 0:
+            sys.stderr.write(out)
+        if p.returncode != 0:
+            failed = f"nvcc failed ({p.returncode}): {' '.join(cmd)}"
+        else:
+            os.replace(tmp, obj)
+    if failed:
+        raise RuntimeError(failed)
+    tmp = LIB + f".tmp{os.getpid()}"
+    cmd = [_nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objects]
     r = subprocess.run(cmd, capture_output=True, text=True)
-    if verbose or r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
     if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError(f"nvcc failed ({r.returncode}): {' '.join(cmd)}")
     os.replace(tmp, LIB)
     return LIB

@@ -23,6 +23,7 @@
 
 #include "l4moe.h"
 #include "finish.cuh"
+#include "launch.cuh"
 #include "moe_gemm.cuh"
 #include "permute.cuh"
 #include "quant.cuh"
@@ -290,41 +291,6 @@ cudaEvent_t take_event(l4moe_handle* h) {
     return e;
 }
 
-// Every kernel goes out with programmatic stream serialisation: it may begin
-// launching while the previous kernel of the stream finishes, and waits for
-// it (pdl_enter) before touching memory, which hides the launch gaps of the
-// short kernels of a small batch.  Launch errors are left for
-// cudaGetLastError, like a <<<>>> launch.
-// cluster_z > 0 also launches the grid as clusters of (1, 1, cluster_z).
-template <typename... KArgs, typename... Args>
-void launch_kc(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-               unsigned cluster_z, Args&&... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 1;
-    if (cluster_z > 0) {
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = 1;
-        attr[1].val.clusterDim.y = 1;
-        attr[1].val.clusterDim.z = cluster_z;
-        cfg.numAttrs = 2;
-    }
-    cfg.attrs = attr;
-    cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-
-template <typename... KArgs, typename... Args>
-void launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-              Args&&... args) {
-    launch_kc(kernel, grid, block, smem, st, 0u, std::forward<Args>(args)...);
-}
-
 // Event pair around one launch when timing is enabled.
 struct LaunchTimer {
     l4moe_handle* h;
@@ -437,28 +403,6 @@ l4moe_status ensure_weight_maps(l4moe_handle* h, const void* const* Wgu, const v
     h->key_sgu = Wsgu;
     h->key_sdn = Wsdn;
     return L4MOE_OK;
-}
-
-template <typename K>
-void set_smem_attr(K kernel, size_t bytes) {
-    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
-// Raise a kernel's dynamic shared-memory limit once per device: the
-// attribute belongs to the kernel's instance in each device's context, so a
-// process that runs layers on several GPUs sets it on each.  `done` holds
-// one bit per device index (devices 64 and up set it on every call).
-template <typename K>
-void ensure_smem_attr(std::atomic<uint64_t>& done, K kernel, size_t bytes) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
-        set_smem_attr(kernel, bytes);
-        return;
-    }
-    const uint64_t bit = 1ull << dev;
-    if (done.load(std::memory_order_acquire) & bit) return;
-    set_smem_attr(kernel, bytes);
-    done.fetch_or(bit, std::memory_order_acq_rel);
 }
 
 template <typename ET, int NT, int TPT, int NG>
@@ -984,6 +928,14 @@ l4moe_status static_workspace(l4moe_handle* h, uint8_t** out) {
 }
 
 }  // namespace
+
+l4moe_status l4moe::op_fail(l4moe_status s, const char* msg) noexcept {
+    try {
+        g_create_error = msg;
+    } catch (...) {  // no memory for the message: the status still tells
+    }
+    return s;
+}
 
 extern "C" {
 

@@ -1,0 +1,180 @@
+"""The losses that train a router, and the per-expert counts of its choices.
+
+    r = router_loss(logits, k, balance=1e-2, z=1e-3, mask=mask)
+    r.loss, r.balance, r.z    fp32 scalars on the device
+    r.counts                  int32 [E]: entries that chose each expert
+    r.rows                    fp32 scalar: the counted rows
+    r.grad(upstream)          the gradient of the logits
+
+For the n counted rows (kept by the mask, and with a logit other than -inf),
+f_e = counts_e / (k n) and share_te = softmax_e(logits_t) (score="softmax") or
+sigmoid(logits_te) / sum_j sigmoid(logits_tj) (score="sigmoid"):
+
+    balance = E sum_e f_e mean_t(share_te)
+    z       = mean_t(logsumexp(logits_t)^2)
+    loss    = balance_weight balance + z_weight z
+
+Each row chooses its k largest logits as the layer's router does (the lower
+index first among equal ones), or idx [T, k] holds the choices: those of a
+layer that has run (`layer.routing()["idx"]`), of a router with its bias, or
+with dropped entries (any index outside [0, E)).
+
+Where the logits take part in autograd (a leaf or the output of the router's
+product), `r.loss` has their gradient: `(task_loss + r.loss).backward()`.
+The other values carry none.  One pass reads the logits for the values, one
+more for the gradient; everything runs in the library's CUDA kernels on the
+caller's stream, with no host synchronisation.
+"""
+from __future__ import annotations
+
+import torch
+
+from .binding import ELEMS, check_op, load_library, op_stream
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+MAX_EXPERTS = 256
+MAX_K = 4
+
+
+def _check(logits, k, score, mask, idx):
+    if logits.dim() != 2:
+        raise ValueError(f"l4moe: logits must be [T, E], got shape {tuple(logits.shape)}")
+    T, E = logits.shape
+    if logits.dtype not in ELEMS:
+        raise ValueError(f"l4moe: logits have dtype {logits.dtype}, expected float32, bfloat16 or float16")
+    if not 1 <= E <= MAX_EXPERTS:
+        raise ValueError(f"l4moe: {E} experts, expected 1 to {MAX_EXPERTS}")
+    if not 1 <= k <= min(MAX_K, E):
+        raise ValueError(f"l4moe: k = {k}, expected 1 to {min(MAX_K, E)}")
+    if score not in SCORES:
+        raise ValueError(f"l4moe: unknown score {score!r}")
+    _rows(logits, "logits")
+    for t, name, shape, dtype in ((mask, "mask", (T,), torch.bool), (idx, "idx", (T, k), torch.int32)):
+        if t is None:
+            continue
+        if tuple(t.shape) != shape and not (name == "idx" and tuple(t.shape) == (T * k,)):
+            raise ValueError(f"l4moe: {name} has shape {tuple(t.shape)}, expected {shape}")
+        if t.dtype != dtype:
+            raise ValueError(f"l4moe: {name} has dtype {t.dtype}, expected {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"l4moe: {name} must be contiguous")
+        if t.device != logits.device:
+            raise ValueError(f"l4moe: {name} is on {t.device}, logits on {logits.device}")
+    if not logits.is_cuda:
+        raise ValueError("l4moe: logits must be a CUDA tensor")
+
+
+def _rows(t, name):
+    """Rows of neighbouring elements, any distance of at least a row apart."""
+    T, E = t.shape
+    if (E > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) < E):
+        raise ValueError(f"l4moe: {name}' rows must be contiguous and must not overlap")
+
+
+def _stride(t):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+class RouterLoss:
+    """The values of one `router_loss` call (views of one device buffer)."""
+
+    def __init__(self, logits, mask, score, result):
+        self._logits, self._mask, self._score, self._result = logits, mask, score, result
+        self._loss = None  # the loss with its autograd history
+
+    @property
+    def loss(self) -> torch.Tensor:
+        return self._result[0] if self._loss is None else self._loss
+
+    @property
+    def balance(self) -> torch.Tensor:
+        return self._result[1]
+
+    @property
+    def z(self) -> torch.Tensor:
+        return self._result[2]
+
+    @property
+    def rows(self) -> torch.Tensor:
+        return self._result[3]
+
+    @property
+    def counts(self) -> torch.Tensor:
+        E = self._logits.shape[1]
+        return self._result[4:4 + E].view(torch.int32)
+
+    def grad(self, upstream: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """The gradient of the logits, times `upstream` (an fp32 device
+        scalar; None: 1), in the logits' type.  `out`: where to write it.
+        The logits (and the mask) must still hold what the call read."""
+        logits = self._logits
+        T, E = logits.shape
+        if upstream is not None:
+            if upstream.dtype != torch.float32 or upstream.numel() != 1 or upstream.device != logits.device:
+                raise ValueError("l4moe: upstream must be one float32 on the logits' device")
+        if out is not None:
+            if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
+                raise ValueError("l4moe: out must have the logits' shape, dtype and device")
+            _rows(out, "out")
+        with op_stream(logits, stream) as st:
+            if out is None:
+                out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+            check_op(load_library().l4moe_router_loss_grad(
+                T, E, logits.data_ptr(), ELEMS[logits.dtype], _stride(logits),
+                None if self._mask is None else self._mask.data_ptr(), self._score, self._result.data_ptr(),
+                None if upstream is None else upstream.data_ptr(), out.data_ptr(), _stride(out), st))
+        return out
+
+
+def _forward(logits, k, balance, z, score, mask, idx, stream) -> RouterLoss:
+    lib = load_library()
+    T, E = logits.shape
+    with op_stream(logits, stream) as st:
+        n = lib.l4moe_router_loss_workspace(T, E)
+        words = 4 + 2 * E + 1
+        # one buffer: the result, then the workspace
+        buf = torch.empty(words + n // 4, dtype=torch.float32, device=logits.device)
+        at = buf.data_ptr()
+        check_op(lib.l4moe_router_loss(
+            T, E, k, logits.data_ptr(), ELEMS[logits.dtype], _stride(logits), None if mask is None else mask.data_ptr(),
+            None if idx is None else idx.data_ptr(), SCORES[score], balance, z, at, at + 4 * words, n, st))
+    return RouterLoss(logits, mask, SCORES[score], buf)
+
+
+class _Loss(torch.autograd.Function):
+    """The loss as a function of the logits."""
+
+    @staticmethod
+    def forward(ctx, logits, args, box):
+        r = _forward(logits.detach(), *args)
+        box.append(r)
+        ctx.save_for_backward(logits, r._result)
+        ctx.mask, ctx.score = r._mask, r._score
+        return r._result[0].clone()
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, upstream):
+        logits, result = ctx.saved_tensors
+        return RouterLoss(logits.detach(), ctx.mask, ctx.score, result).grad(upstream.contiguous()), None, None
+
+
+def router_loss(logits: torch.Tensor, k: int = 1, *, balance: float = 1e-2, z: float = 1e-3, score: str = "softmax",
+                mask: torch.Tensor | None = None, idx: torch.Tensor | None = None, stream=None) -> RouterLoss:
+    """Balance loss, z loss and per-expert counts of a router's logits.
+
+    logits [T, E] fp32, bf16 or fp16 (rows of neighbouring elements; row
+    strides are taken as they are), 1 <= E <= 256, 1 <= k <= min(4, E);
+    mask bool [T]: the rows that count (None: all); idx int32 [T, k]: the
+    choices (None: each row's k largest logits).  balance and z are the
+    weights of the two losses in `loss`."""
+    k = int(k)
+    _check(logits, k, score, mask, idx)
+    args = (k, float(balance), float(z), score, mask, idx, stream)
+    if not (logits.requires_grad and torch.is_grad_enabled()):
+        return _forward(logits, *args)
+    box = []
+    loss = _Loss.apply(logits, args, box)
+    r = box[0]
+    r._loss = loss
+    return r
