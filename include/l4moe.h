@@ -114,6 +114,9 @@ typedef enum {
     L4MOE_INT4 = 4
 } l4moe_dtype;
 
+/* Element types of group scales and of the operators without a handle. */
+typedef enum { L4MOE_ELEM_F32 = 0, L4MOE_ELEM_BF16 = 1, L4MOE_ELEM_F16 = 2 } l4moe_elem;
+
 typedef struct {
     int d_model;      /* d  : model width (KerasFormers "Llama 4": embed_dim)       */
     int expert_ffn;   /* F  : routed expert width (Maverick table: d_expert)       */
@@ -180,6 +183,21 @@ L4MOE_API l4moe_status l4moe_set_weight_scales(l4moe_handle *h, const float *con
 L4MOE_API l4moe_status l4moe_set_fp8_scales(l4moe_handle *h, const float *const *s_gate_up,
                                   const float *const *s_down, const float *ss_gate_up,
                                   const float *ss_down);
+
+/* int4 weights only: group scales instead of column scales.  The weight of
+ * input row k and column n is q[k, n] * s[k / group, n]: s_gate_up / s_down
+ * are HOST arrays of E device pointers to [ceil(d / group), 2F] /
+ * [ceil(F / group), d] matrices of `type`, ss_gate_up [ceil(d / group), 2Fs]
+ * and ss_down [ceil(Fs / group), d] the shared expert's; group a multiple of
+ * 32; the pointers 16-byte aligned, kept like l4moe_set_weight_scales's (the
+ * latest of the two calls holds).  The layer's values are those of column
+ * scales otherwise: x in f16 (times a row's power of two), hidden rows in
+ * f16 (L4MOE_ERR_RANGE past it), fp32 sums; no weight is rounded.  Its
+ * products then run for up to 8 rows of an expert at a time (built for the
+ * small batches of decode; longer batches read an expert's weights again for
+ * every 8 rows). */
+L4MOE_API l4moe_status l4moe_set_group_scales(l4moe_handle *h, int group, l4moe_elem type, const void *const *s_gate_up,
+                                    const void *const *s_down, const void *ss_gate_up, const void *ss_down);
 
 /* FP8 activation mode (on = 1; off = 0, the default), E4M3 weights only.
  * superteams.ai "Llama 4" glossary, "Running Llama 4 Yourself": Maverick is
@@ -347,8 +365,6 @@ L4MOE_API uint64_t l4moe_launch_count(const l4moe_handle *h);
  * different streams as long as their outputs and workspaces differ.
  * l4moe_last_error(NULL) has the message of this thread's last refused call. */
 
-typedef enum { L4MOE_ELEM_F32 = 0, L4MOE_ELEM_BF16 = 1, L4MOE_ELEM_F16 = 2 } l4moe_elem;
-
 /* How a logit becomes an expert's share of its token: softmax over the
  * experts, or the sigmoid (the layer's gate) divided by the sum of the
  * token's sigmoids. */
@@ -388,6 +404,26 @@ L4MOE_API l4moe_status l4moe_router_loss(int T, int E, int k, const void *logits
 L4MOE_API l4moe_status l4moe_router_loss_grad(int T, int E, const void *logits, l4moe_elem type, long long ld,
                                     const uint8_t *mask, l4moe_score score, const float *result,
                                     const float *upstream, void *dlogits, long long ldd, void *stream);
+
+/* Products of a few tokens with a 4-bit weight that has one scale per group
+ * of `group` input rows and output column:
+ *   y[t, n] = sum_k x[t, k] q[k, n] scales[k / group, n]
+ * x [T, K] and y [T, N] bf16 or f16 (x_type), 0 <= T <= L4MOE_INT4_MAX_TOKENS;
+ * w [K, N / 2] bytes, the layer's int4 layout (two's-complement nibbles, the
+ * even column in the low one); scales [ceil(K / group), N] of s_type; group a
+ * multiple of 32 (group >= K: one scale per column; the last group may be
+ * short).  Any 1 <= K <= 2^30 and even
+ * 2 <= N <= 2^30; rows of a multiple of 16 columns are read
+ * in wide loads.  Sums are fp32 and the result is rounded once.  Every f16 x
+ * is taken exactly; bf16 rows are divided by a power of two into f16's range,
+ * exact down to 2^-31 of the row's largest magnitude and to 2^-39 of it
+ * below.  A row of x with an infinity or a NaN gives NaN in all its outputs;
+ * the other rows are not touched by it.  w need not differ between calls in
+ * flight; tensors 16-byte aligned, contiguous, on the current device. */
+#define L4MOE_INT4_MAX_TOKENS 64
+L4MOE_API l4moe_status l4moe_int4_matvec(int T, int K, int N, int group, const void *x, l4moe_elem x_type,
+                               const void *w, const void *scales, l4moe_elem s_type, void *y,
+                               void *stream);
 
 /* Message for the handle's last non-OK status ("" if none); h may be NULL
  * for errors of l4moe_create and of the operators without a handle. */

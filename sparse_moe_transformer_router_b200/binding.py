@@ -24,7 +24,7 @@ EXPORTED = ("l4moe_create", "l4moe_destroy", "l4moe_workspace_size", "l4moe_set_
             "l4moe_set_timing", "l4moe_read_timing", "l4moe_kernel_name",
             "l4moe_forward_static", "l4moe_join_host", "l4moe_set_top_k",
             "l4moe_set_weight_scales", "l4moe_selftest_wait", "l4moe_set_act_fp8", "l4moe_get_plan",
-            "l4moe_router_loss_workspace", "l4moe_router_loss", "l4moe_router_loss_grad")
+            "l4moe_set_group_scales", "l4moe_int4_matvec", "l4moe_router_loss_workspace", "l4moe_router_loss", "l4moe_router_loss_grad")
 STATIC_WORKSPACE_BYTES = 32 << 20
 NUM_KERNELS = 6
 
@@ -91,6 +91,8 @@ def load_library():
     lib.l4moe_read_timing.argtypes = [vp, ctypes.POINTER(ctypes.c_double),
                                       ctypes.POINTER(ctypes.c_uint64)]
     f32, i64 = ctypes.c_float, ctypes.c_longlong
+    lib.l4moe_set_group_scales.argtypes = [vp, i32, i32, pvp, pvp, vp, vp]
+    lib.l4moe_int4_matvec.argtypes = [i32, i32, i32, i32, vp, i32, vp, vp, i32, vp, vp]
     lib.l4moe_router_loss_workspace.argtypes = [i32, i32]
     lib.l4moe_router_loss_workspace.restype = sz
     lib.l4moe_router_loss.argtypes = [i32, i32, i32, vp, i32, i64, vp, vp, i32, f32, f32, vp, vp, sz, vp]
@@ -102,7 +104,8 @@ def load_library():
                  "l4moe_get_routing", "l4moe_check_device_status", "l4moe_version",
                  "l4moe_set_timing", "l4moe_read_timing", "l4moe_forward_static",
                  "l4moe_join_host", "l4moe_set_top_k", "l4moe_set_weight_scales", "l4moe_selftest_wait",
-                 "l4moe_set_act_fp8", "l4moe_get_plan", "l4moe_router_loss", "l4moe_router_loss_grad"):
+                 "l4moe_set_act_fp8", "l4moe_get_plan", "l4moe_router_loss", "l4moe_router_loss_grad",
+                 "l4moe_set_group_scales", "l4moe_int4_matvec"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -243,13 +246,50 @@ class L4MoE:
         self._check(self._lib.l4moe_set_router_bias(self._h, _ptr(bias)))
         self._bias = bias
 
-    def set_weight_scales(self, s_gate_up, s_down, ss_gate_up, ss_down):
-        """Per-output-column fp32 scales of E4M3, int8 or int4 weights (device tensors)."""
+    def set_weight_scales(self, s_gate_up, s_down, ss_gate_up, ss_down, group: int = 0):
+        """Scales of E4M3, int8 or int4 weights (device tensors): one fp32 per
+        output column, or (int4, group a multiple of 32) one per `group` input
+        rows and output column: s_gate_up[e] [ceil(d / group), 2F], s_down[e]
+        [ceil(F / group), d], ss_gate_up [ceil(d / group), 2Fs], ss_down
+        [ceil(Fs / group), d], all of one type (fp32, bf16 or fp16)."""
+        if group:
+            return self._set_group_scales(s_gate_up, s_down, ss_gate_up, ss_down, int(group))
         a, b = _ptr_array(s_gate_up), _ptr_array(s_down)
         self._check(self._lib.l4moe_set_weight_scales(self._h, a, b, _ptr(ss_gate_up), _ptr(ss_down)))
         self._scales = (list(s_gate_up), list(s_down), ss_gate_up, ss_down)
 
     set_fp8_scales = set_weight_scales
+
+    def _set_group_scales(self, s_gate_up, s_down, ss_gate_up, ss_down, group):
+        if self.dtype != "int4":
+            raise ValueError(f"l4moe: group scales apply to int4 weights, not {self.dtype}")
+        if group < 32 or group % 32:
+            raise ValueError(f"l4moe: group = {group}, expected a multiple of 32")
+        d, F, Fs, E = self.d_model, self.expert_ffn, self.shared_ffn, self.num_experts
+        if len(s_gate_up) != E or len(s_down) != E:
+            raise ValueError(f"l4moe: expected scales of {E} experts, got {len(s_gate_up)} / {len(s_down)}")
+        if ss_gate_up is None or ss_gate_up.dtype not in ELEMS:
+            raise ValueError("l4moe: ss_gate_up is required, in float32, bfloat16 or float16")
+        dtype = ss_gate_up.dtype
+        rows = lambda n: -(-n // group)  # noqa: E731
+        named = [(s_gate_up[e], f"s_gate_up[{e}]", (rows(d), 2 * F)) for e in range(E)]
+        named += [(s_down[e], f"s_down[{e}]", (rows(F), d)) for e in range(E)]
+        named += [(ss_gate_up, "ss_gate_up", (rows(d), 2 * Fs)), (ss_down, "ss_down", (rows(Fs), d))]
+        for t, name, shape in named:
+            _expect(t, name, shape, dtype)
+        for t, name, _ in named:
+            _where(t, name)
+            if t.device != self.device:
+                raise ValueError(f"l4moe: {name} is on {t.device}, the layer on {self.device}")
+        self._check(self._lib.l4moe_set_group_scales(self._h, group, ELEMS[dtype], _ptr_array(s_gate_up),
+                                                     _ptr_array(s_down), _ptr(ss_gate_up), _ptr(ss_down)))
+        self._scales = (list(s_gate_up), list(s_down), ss_gate_up, ss_down)
+
+    def bind(self, W_router, W_gate_up, W_down, Ws_gate_up, Ws_down) -> "BoundLayer":
+        """The layer with its weights: checked once and held, so that a call
+        passes the tokens alone (decode, where checking 2 E weight tensors per
+        call would cost as much as the layer)."""
+        return BoundLayer(self, W_router, W_gate_up, W_down, Ws_gate_up, Ws_down)
 
     def _weights(self, W_gate_up, W_down, Ws_gate_up, Ws_down):
         """Pointer arrays of the expert weights; shapes, dtypes, devices and
@@ -310,6 +350,18 @@ class L4MoE:
         self._check(self._lib.l4moe_forward(self._h, T, _ptr(x), _ptr(W_router), gu, dn,
                                             _ptr(Ws_gate_up), _ptr(Ws_down), _ptr(out),
                                             _stream_handle(stream)))
+        self.last_T = T
+        return out
+
+    def _forward_bound(self, x, bound, out, stream):
+        T = self._check_io(x, bound.W_router, out)
+        if x.device != self.device or (out is not None and out.device != self.device):
+            raise ValueError(f"l4moe: x or out is not on the layer's device {self.device}")
+        if out is None:
+            out = torch.empty((T, self.d_model), dtype=x.dtype, device=x.device)
+        gu, dn = bound.arrays
+        self._check(self._lib.l4moe_forward(self._h, T, _ptr(x), bound.router_ptr, gu, dn, bound.shared[0],
+                                            bound.shared[1], _ptr(out), _stream_handle(stream)))
         self.last_T = T
         return out
 
@@ -404,3 +456,25 @@ class L4MoE:
     @property
     def launch_count(self) -> int:
         return int(self._lib.l4moe_launch_count(self._h))
+
+
+class BoundLayer:
+    """An `L4MoE` with the weights it runs (`L4MoE.bind`).  The tensors are
+    held, not copied: values written into them later are used, and moving
+    their storage (`.data = `, `.set_()`) needs a new bind."""
+
+    def __init__(self, layer: L4MoE, W_router, W_gate_up, W_down, Ws_gate_up, Ws_down):
+        self.layer = layer
+        if layer.num_experts > 0:
+            _expect(W_router, "W_router", (layer.d_model, layer.num_experts), _ACT_DTYPE[layer.dtype])
+            _where(W_router, "W_router")
+        W_gate_up, W_down = list(W_gate_up or ()), list(W_down or ())
+        self.arrays = layer._weights(W_gate_up, W_down, Ws_gate_up, Ws_down)
+        self.W_router = W_router
+        self.router_ptr = _ptr(W_router)
+        self.shared = (_ptr(Ws_gate_up), _ptr(Ws_down))
+        self._keep = (W_gate_up, W_down, Ws_gate_up, Ws_down)
+
+    def forward(self, x, out=None, stream=None):
+        """`L4MoE.forward` with the bound weights."""
+        return self.layer._forward_bound(x, self, out, stream)

@@ -23,6 +23,7 @@
 
 #include "l4moe.h"
 #include "finish.cuh"
+#include "int4_mv.cuh"
 #include "launch.cuh"
 #include "moe_gemm.cuh"
 #include "permute.cuh"
@@ -233,6 +234,8 @@ struct l4moe_handle {
     std::vector<const float*> s_gu, s_dn;
     const float* ss_gu = nullptr;
     const float* ss_dn = nullptr;
+    int group = 0;  // rows per scale of int4 weights (l4moe_set_group_scales); 0: column scales
+    l4moe_elem group_type = L4MOE_ELEM_F32;
     const float** d_scales = nullptr;  // device [2][E+1] scale pointers (gate/up, down)
     bool scales_dirty = false;
     // host copy of that table, the source of every upload: sized once at
@@ -456,6 +459,32 @@ void launch_gemm(int grid, const BMaps& bm, const GemmArgs& a, cudaStream_t st, 
     launch_gemm_pair<MODE, ET, WQ>(grid, bm, a, bm, a, st, small);
 }
 
+// The weights of one forward whose experts have group scales: the pointers
+// themselves (the launches carry them).
+struct ExpertWeights {
+    const void* const* gate_up;
+    const void* const* down;
+    const void *shared_gate_up, *shared_down;
+};
+
+template <typename ST, bool GATE_UP>
+void launch_experts_t(dim3 grid, cudaStream_t st, const GroupTable* tab, int E, int group, const mv::Experts& ptrs,
+                      const mv::Rows& rows) {
+    constexpr size_t smem = mv::smem_bytes<1>();
+    static std::atomic<uint64_t> attr_done{0};
+    ensure_smem_attr(attr_done, mv::experts_kernel<ST, GATE_UP>, smem);
+    launch_kc(mv::experts_kernel<ST, GATE_UP>, grid, dim3(mv::kThreads), smem, st, grid.z > 1 ? grid.z : 0u, tab, E,
+              group, ptrs, rows);
+}
+
+template <bool GATE_UP>
+void launch_experts(l4moe_elem type, dim3 grid, cudaStream_t st, const GroupTable* tab, int E, int group,
+                    const mv::Experts& ptrs, const mv::Rows& rows) {
+    if (type == L4MOE_ELEM_F32) launch_experts_t<float, GATE_UP>(grid, st, tab, E, group, ptrs, rows);
+    else if (type == L4MOE_ELEM_BF16) launch_experts_t<__nv_bfloat16, GATE_UP>(grid, st, tab, E, group, ptrs, rows);
+    else launch_experts_t<__half, GATE_UP>(grid, st, tab, E, group, ptrs, rows);
+}
+
 // The launch sequence of one forward.  w / ws_tokens: the workspace and the
 // token count its layout was made for; maps: device array of the 2(E+1)
 // weight descriptors.
@@ -466,7 +495,8 @@ void launch_gemm(int grid, const BMaps& bm, const GemmArgs& a, cudaStream_t st, 
 template <typename ET, int WQ = kWqNone>
 l4moe_status run_layer(l4moe_handle* h, int T, const void* x, const void* Wr, const void* Wsgu,
                        const void* Wsdn, void* out, cudaStream_t st, uint8_t* w, int ws_tokens,
-                       const CUtensorMap* maps, const float* const* scales = nullptr) {
+                       const CUtensorMap* maps, const float* const* scales = nullptr,
+                       const ExpertWeights* grouped = nullptr) {
     constexpr bool FP8W = WQ != kWqNone;  // coded weights with per-column scales
     constexpr bool ACT8 = WQ == kWqAct8;  // and E4M3 token rows (FP8 activation mode)
     const l4moe_params& p = h->p;
@@ -539,7 +569,9 @@ l4moe_status run_layer(l4moe_handle* h, int T, const void* x, const void* Wr, co
     const void* hrm = F > 0 ? hdr : hds;
     const int Fr = F > 0 ? F : Fs;
     const size_t gsz = sizeof(GT);
-    if (!act(&m_x, adt, x, d, 64, sizeof(ET)) || !act_r(&bm_gu.routed, gdt, xg, d, rb, gsz) ||
+    // (grouped: the experts' products read their rows directly, and the small-batch routing x)
+    if (grouped ? (T > kSmallMaxTokens && !act(&m_x, adt, x, d, 64, sizeof(ET)))
+        : !act(&m_x, adt, x, d, 64, sizeof(ET)) || !act_r(&bm_gu.routed, gdt, xg, d, rb, gsz) ||
         !act_r(&bm_gu.routed_small, gdt, xg, d, rs, gsz) || !act(&bm_gu.shared, gdt, xs, d, rb, gsz) ||
         !act(&bm_gu.shared_small, gdt, xs, d, rs, gsz) || !act_r(&bm_dn.routed, ddt, hrm, Fr, rb, dsz) ||
         !act_r(&bm_dn.routed_small, ddt, hrm, Fr, rs, dsz) || !act(&bm_dn.shared, ddt, hds, Fs, rb, dsz) ||
@@ -675,6 +707,62 @@ l4moe_status run_layer(l4moe_handle* h, int T, const void* x, const void* Wr, co
                      (const int32_t*)nullptr, (const int32_t*)nullptr, 1, 0, (int32_t*)nullptr, tokscale);
             t_rows.stop();
             L4MOE_CHECK_LAUNCH("row conversion launch");
+        }
+    }
+
+    if constexpr (WQ == kWqInt4) {
+        if (grouped) {
+            // experts with group scales: gate/up and down as products of up to
+            // 8 rows, the sums of a token added by the down finish
+            const bool has = E > 0;
+            mv::Rows R{};
+            R.x[0] = xg, R.x[1] = x16;
+            R.K[0] = R.K[1] = d;
+            R.N[0] = 2 * F, R.N[1] = 2 * Fs;
+            R.scale[0] = gslot, R.scale[1] = tokscale;
+            R.h[0] = hr, R.h[1] = hs;
+            R.err = err;
+            mv::Experts ptrs;
+            auto fill = [&](const void* const* q, const void* qs, int first) {
+                for (int e = 0; e < E; ++e) {
+                    ptrs.q[e] = static_cast<const uint8_t*>(q[e]);
+                    ptrs.s[e] = h->scale_tab[first + e];
+                }
+                ptrs.q[E] = static_cast<const uint8_t*>(qs);
+                ptrs.s[E] = h->scale_tab[first + E];
+            };
+            // tiles of 8 rows: every routed one holds an entry
+            const int units = (has ? std::min(Tv, std::min(E, Tv) + Tv / 8) : 0) + (T + 7) / 8;
+            if (units > 65535) return fail(h, L4MOE_ERR_ARG, "batch too long for experts with group scales");
+            const int gt = (std::max(has ? F : 0, Fs) + 127) / 128, dt = (d + mv::kCols - 1) / mv::kCols;
+            const int sg = mv::slices((long long)gt * units, d, h->sms);
+            const int sd = mv::slices((long long)dt * units, has ? std::min(F, Fs) : Fs, h->sms);
+            fill(grouped->gate_up, grouped->shared_gate_up, 0);
+            {
+                LaunchTimer t_gu(h, 3, st);
+                launch_experts<true>(h->group_type, dim3(gt, units, sg), st, tab_gu, E, h->group, ptrs, R);
+                t_gu.stop();
+                L4MOE_CHECK_LAUNCH("grouped gate/up launch");
+            }
+            fill(grouped->down, grouped->shared_down, E + 1);
+            float* part = reinterpret_cast<float*>(w + L.part);
+            R.x[0] = hr, R.x[1] = hs;
+            R.K[0] = F, R.K[1] = Fs;
+            R.N[0] = R.N[1] = d;
+            R.part[0] = part, R.part[1] = part + (size_t)(has ? Tv : 0) * d;
+            R.perm = perm;
+            LaunchTimer t_dn(h, 4, st);
+            launch_experts<false>(h->group_type, dim3(dt, units, sd), st, tab_dn, E, h->group, ptrs, R);
+            L4MOE_CHECK_LAUNCH("grouped down launch");
+            const long long n = (long long)T * d;
+            launch_k(down_finish_kernel<ET>, dim3((int)std::min<long long>((n / 4 + 255) / 256, 8LL * h->sms)),
+                     dim3(256), 0, st, (const float*)part, (long long)Tv * d, has ? 1 : 0, (const float*)R.part[1],
+                     (long long)T * d, 1, k, d, n, static_cast<ET*>(out), (unsigned*)nullptr);
+            t_dn.stop();
+            L4MOE_CHECK_LAUNCH("down finish launch");
+            h->last_plan = l4moe_plan{sg, sd, (has && T <= kSmallMaxTokens) ? 1 : 0, 0, 0, 0};
+            h->last_T = T;
+            return L4MOE_OK;
         }
     }
 
@@ -876,6 +964,11 @@ l4moe_status forward_impl(l4moe_handle* h, int T, const void* x, const void* Wr,
                           const void* Wsdn, void* out, cudaStream_t st) {
     l4moe_status s;
     if ((s = ensure_workspace(h, T)) != L4MOE_OK) return s;
+    if (h->group) {
+        const ExpertWeights g{Wgu, Wdn, Wsgu, Wsdn};
+        return run_layer<__nv_bfloat16, kWqInt4>(h, T, x, Wr, Wsgu, Wsdn, out, st, h->ws, h->ws_tokens, nullptr,
+                                                 nullptr, &g);
+    }
     if ((s = ensure_weight_maps(h, Wgu, Wdn, Wsgu, Wsdn, st)) != L4MOE_OK) return s;
     if (coded8(h->p.dtype) && (s = ensure_scales(h, st)) != L4MOE_OK) return s;
     switch (h->p.dtype) {
@@ -948,8 +1041,9 @@ l4moe_status l4moe_forward_static(l4moe_handle* h, int T, const void* x, const v
     const int E = h->p.num_experts;
     const bool fp8 = coded8(h->p.dtype);
     const size_t ws_bytes = (ws_layout(h->p, T, h->sms, h->top_k, h->act8).device_total + 255) & ~size_t(255);
-    const size_t maps_bytes = sizeof(CUtensorMap) * 2 * (E + 1);
-    const size_t scales_bytes = fp8 ? sizeof(float*) * 2 * (E + 1) : 0;
+    // (experts with group scales: the launches carry the pointers)
+    const size_t maps_bytes = h->group ? 0 : sizeof(CUtensorMap) * 2 * (E + 1);
+    const size_t scales_bytes = fp8 && !h->group ? sizeof(float*) * 2 * (E + 1) : 0;
     if (ws_bytes + maps_bytes + scales_bytes > L4MOE_STATIC_WORKSPACE_BYTES) {
         char msg[200];
         snprintf(msg, sizeof msg,
@@ -959,19 +1053,22 @@ l4moe_status l4moe_forward_static(l4moe_handle* h, int T, const void* x, const v
     }
     uint8_t* base = nullptr;
     if ((s = static_workspace(h, &base)) != L4MOE_OK) return s;
-    if ((s = encode_weight_maps(h, W_gate_up, W_down, Ws_gate_up, Ws_down)) != L4MOE_OK) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     CUtensorMap* maps = reinterpret_cast<CUtensorMap*>(base + ws_bytes);
     // every call shares the array: upload this call's descriptors and clear
     // the state a forward expects to start at zero
-    cudaError_t e = cudaMemcpyAsync(maps, h->h_maps.data(), maps_bytes, cudaMemcpyHostToDevice, st);
-    if (e != cudaSuccess) return cuda_fail(h, e, "static descriptor upload");
+    cudaError_t e = cudaSuccess;
+    if (!h->group) {
+        if ((s = encode_weight_maps(h, W_gate_up, W_down, Ws_gate_up, Ws_down)) != L4MOE_OK) return s;
+        e = cudaMemcpyAsync(maps, h->h_maps.data(), maps_bytes, cudaMemcpyHostToDevice, st);
+        if (e != cudaSuccess) return cuda_fail(h, e, "static descriptor upload");
+    }
     // the error word, the routing kernels' ticket and the fused GEMM's two
     // tile counters that follow it
     e = cudaMemsetAsync(base + ws_layout(h->p, T, h->sms, h->top_k, h->act8).err, 0, 4 * sizeof(unsigned), st);
     if (e != cudaSuccess) return cuda_fail(h, e, "static error word clear");
     const float* const* scales = nullptr;
-    if (fp8) {  // the scale-pointer table of 8-bit weights follows the descriptors
+    if (scales_bytes) {  // the scale-pointer table of 8-bit weights follows the descriptors
         scales = reinterpret_cast<const float* const*>(base + ws_bytes + maps_bytes);
         e = cudaMemcpyAsync(const_cast<const float**>(scales), h->scale_tab.data(), scales_bytes,
                             cudaMemcpyHostToDevice, st);
@@ -979,7 +1076,11 @@ l4moe_status l4moe_forward_static(l4moe_handle* h, int T, const void* x, const v
     }
     const unsigned timing = h->timing;  // event timing would create events: off here
     h->timing = 0;
-    if (h->p.dtype == L4MOE_F32)
+    const ExpertWeights grouped{W_gate_up, W_down, Ws_gate_up, Ws_down};
+    if (h->group)
+        s = run_layer<__nv_bfloat16, kWqInt4>(h, T, x, W_router, Ws_gate_up, Ws_down, out, st, base, T, nullptr,
+                                              nullptr, &grouped);
+    else if (h->p.dtype == L4MOE_F32)
         s = run_layer<float>(h, T, x, W_router, Ws_gate_up, Ws_down, out, st, base, T, maps);
     else if (h->p.dtype == L4MOE_FP8_E4M3 && h->act8)
         s = run_layer<__nv_bfloat16, kWqAct8>(h, T, x, W_router, Ws_gate_up, Ws_down, out, st, base, T, maps,
@@ -1156,6 +1257,37 @@ l4moe_status l4moe_set_weight_scales(l4moe_handle* h, const float* const* s_gate
     h->ss_dn = ss_down;
     fill_scale_table(h);
     h->scales_dirty = true;
+    h->group = 0;
+    return L4MOE_OK;
+}
+
+l4moe_status l4moe_set_group_scales(l4moe_handle* h, int group, l4moe_elem type, const void* const* s_gate_up,
+                                    const void* const* s_down, const void* ss_gate_up, const void* ss_down) {
+    if (!h) return L4MOE_ERR_ARG;
+    if (h->p.dtype != L4MOE_INT4) return fail(h, L4MOE_ERR_DTYPE, "group scales apply to int4 weights only");
+    if (type != L4MOE_ELEM_F32 && type != L4MOE_ELEM_BF16 && type != L4MOE_ELEM_F16)
+        return fail(h, L4MOE_ERR_DTYPE, "unknown scale type");
+    if (group < 32 || group % 32) return fail(h, L4MOE_ERR_ARG, "group must be a multiple of 32");
+    const int E = h->p.num_experts;
+    if (!ss_gate_up || !ss_down || (E > 0 && (!s_gate_up || !s_down)))
+        return fail(h, L4MOE_ERR_ARG, "null scale pointer");
+    bool aligned = aligned16(ss_gate_up) && aligned16(ss_down);
+    for (int e = 0; e < E; ++e) {
+        if (!s_gate_up[e] || !s_down[e]) return fail(h, L4MOE_ERR_ARG, "null expert scale pointer");
+        aligned = aligned && aligned16(s_gate_up[e]) && aligned16(s_down[e]);
+    }
+    if (!aligned) return fail(h, L4MOE_ERR_ALIGN, "scale pointer not 16-byte aligned");
+    // the table of the column scales, holding the groups' matrices
+    const float* const* gu = reinterpret_cast<const float* const*>(s_gate_up);
+    const float* const* dn = reinterpret_cast<const float* const*>(s_down);
+    h->s_gu.assign(gu, gu + E);
+    h->s_dn.assign(dn, dn + E);
+    h->ss_gu = static_cast<const float*>(ss_gate_up);
+    h->ss_dn = static_cast<const float*>(ss_down);
+    fill_scale_table(h);
+    h->scales_dirty = true;
+    h->group = group;
+    h->group_type = type;
     return L4MOE_OK;
 }
 

@@ -236,6 +236,23 @@ def generate(cfg: LayerConfig, seed: int = 0, device="cpu", experts=None) -> Lay
                        ss_gu if scaled else None, ss_dn if scaled else None)
 
 
+def quantize_int4_groups(w: torch.Tensor, group: int, dtype=torch.float32):
+    """Symmetric int4 quantisation of an fp32 [K, N] weight with one scale per
+    `group` rows (the last group may be short) and column: scale = max |w| / 7
+    over the group, held in `dtype`, q = round(w / scale) to nearest even,
+    clamped to [-7, 7].  Returns (packed uint8 [K, N / 2], scales
+    [ceil(K / group), N])."""
+    K, N = w.shape
+    rows = -(-K // group)
+    padded = torch.zeros((rows * group, N), dtype=w.dtype, device=w.device)
+    padded[:K] = w
+    amax = padded.view(rows, group, N).abs().amax(dim=1)
+    scale = torch.where(amax > 0, amax / INT4_MAX, torch.ones_like(amax)).to(dtype)
+    each = scale.to(w.dtype).repeat_interleave(group, dim=0)[:K]
+    q = torch.round(w / each).clamp_(-INT4_MAX, INT4_MAX).to(torch.int8)
+    return pack_int4(q), scale
+
+
 # E4M3 code sets for layers that exercise the weight widening: every finite
 # code (0x7F / 0xFF are NaN), and the zero and subnormal codes (exponent
 # field 0) alone.
