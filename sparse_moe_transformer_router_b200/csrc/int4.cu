@@ -22,7 +22,7 @@ struct Call {
 
 template <int NT8, typename XT, typename ST, bool VEC>
 cudaError_t launch(const Call& c) {
-    constexpr size_t smem = mv::smem_bytes<NT8>();
+    constexpr size_t smem = mv::Cfg<NT8, ST>::SMEM;
     static std::atomic<uint64_t> attr_done{0};
     ensure_smem_attr(attr_done, mv::int4_matvec_kernel<NT8, XT, ST, VEC>, smem);
     const int tiles = (c.N + mv::kCols - 1) / mv::kCols, tt = (c.T + NT8 * 8 - 1) / (NT8 * 8);

@@ -40,6 +40,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+#include <cstring>
 #include <type_traits>
 
 #include "schedule.cuh"
@@ -51,21 +52,28 @@ namespace mv {
 constexpr unsigned kErrF16Range = 1u << 4;  // DEV_ERR_F16_RANGE of the layer's error word
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kCols = 256;       // columns of a CTA: two halves of 128
 constexpr int kQuarters = 4;     // warps of a half, each on a quarter of a chunk
 constexpr int kBlock = 32;       // rows of a block (scale groups are multiples of it)
-constexpr int kChunk = 2048;     // rows of x staged at a time
+constexpr int kChunk = 1024;     // rows of x staged at a time
 constexpr int kXStride = kChunk + 32;  // halves; 64 bytes past a multiple of 128: the two
                                        // tokens of a quarter-warp's load use other banks
 
-// Dynamic shared memory for NT8 * 8 tokens: x and its block sums, then (in
-// the same place) the warps' sums.
-template <int NT8>
-__host__ __device__ constexpr size_t smem_bytes() {
-    const size_t x = sizeof(__half) * NT8 * 8 * kXStride + sizeof(float) * (kChunk / kBlock) * NT8 * 8;
-    const size_t red = sizeof(float) * kQuarters * NT8 * 8 * kCols;
-    return x > red ? x : red;
-}
+// A warp's ring of weight blocks: 8 bytes per row and lane, each lane's own,
+// then the block's scales of the warp's 128 columns.
+template <int NT8, typename ST>
+struct Cfg {
+    static constexpr int WORDS = 8 * 32 * 8;
+    static constexpr int STAGE = WORDS + 128 * (int)sizeof(ST);
+    // two CTAs per SM want at most 113 KB each
+    static constexpr int STAGES = (NT8 == 2 && sizeof(ST) == 4) ? 3 : 4;
+    static constexpr int X = (int)sizeof(__half) * NT8 * 8 * kXStride;
+    static constexpr int BIAS = (int)sizeof(float) * (kChunk / kBlock) * NT8 * 8;
+    static constexpr int RING = kWarps * STAGES * STAGE;
+    static constexpr int RED = (int)sizeof(float) * kQuarters * NT8 * 8 * kCols;  // over all of it
+    static constexpr int SMEM = X + BIAS + RING > RED ? X + BIAS + RING : RED;
+};
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -101,56 +109,51 @@ struct Weight {
     int K, group;
 };
 
-// The 8 words (two per row) of a thread's 8 rows: rows past K give zeros (x
-// is zero there), columns past the limit too.
-template <bool VEC>
-__device__ __forceinline__ void load_words(uint2 (&w)[8], const uint8_t* q, long long row_bytes, int row, int K, int col,
-                                           int limit) {
+// Issue one block's loads into a stage: this lane's 8 rows of 8 bytes (16
+// columns), and its part of the scales of the warp's columns.  Rows past K
+// and columns past the limit are zeros.  VEC: asynchronous copies (rows of a
+// multiple of 16 columns); else plain loads, byte by byte.
+template <typename ST, bool VEC>
+__device__ __forceinline__ void issue_block(uint8_t* stage, const Weight<ST>& W, int row, int col, int limit, int lane) {
+    const int t = lane & 3, g = lane >> 2;
+    const int r0 = row + 8 * t;
+    const ST* s = W.s + (long long)(row / W.group) * W.N;
+    constexpr int WORDS = Cfg<1, ST>::WORDS;
+    constexpr int SB = 4 * (int)sizeof(ST);  // scale bytes of a lane: 4 columns
     if constexpr (VEC) {
-        const uint2* p = reinterpret_cast<const uint2*>(q + row * row_bytes + (col >> 1));
-        const long long step = row_bytes >> 3;
+        const bool in = col < limit;
+        const uint8_t* p = W.q + (in ? r0 * W.row_bytes + (col >> 1) : 0);
+        const uint32_t dst = op::smem_u32(stage) + lane * 8;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            w[i] = make_uint2(0u, 0u);
-            if (row + i < K && col < limit) w[i] = __ldg(p + i * step);
+            const bool ok = in && r0 + i < W.K;
+            op::cp_async<8>(dst + i * 256, ok ? p + i * W.row_bytes : W.q, ok);
         }
+        op::cp_async<SB>(op::smem_u32(stage) + WORDS + g * 16 * (int)sizeof(ST) + t * SB, in ? s + col + 4 * t : W.s, in);
     } else {
         const int nb = min(8, (limit - col + 1) >> 1);  // limit and col are even: whole bytes
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             uint32_t lo = 0u, hi = 0u;
-            if (row + i < K) {
-                const uint8_t* p = q + (row + i) * row_bytes + (col >> 1);
+            if (r0 + i < W.K) {
+                const uint8_t* p = W.q + (r0 + i) * W.row_bytes + (col >> 1);
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     if (b < nb) lo |= (uint32_t)__ldg(p + b) << (8 * b);
                     if (4 + b < nb) hi |= (uint32_t)__ldg(p + 4 + b) << (8 * b);
                 }
             }
-            w[i] = make_uint2(lo, hi);
+            reinterpret_cast<uint2*>(stage)[i * 32 + lane] = make_uint2(lo, hi);
         }
-    }
-}
-
-template <typename ST, bool VEC>
-__device__ __forceinline__ void load_scales(float (&sc)[16], const ST* s, int col, int limit) {
-    if constexpr (VEC) {
-        constexpr int V = 16 / (int)sizeof(ST);
-        if (col < limit) {
+        ST* d = reinterpret_cast<ST*>(stage + WORDS) + g * 16 + t * 4;
 #pragma unroll
-            for (int i = 0; i < 16 / V; ++i) {
-                ST tmp[V];
-                *reinterpret_cast<uint4*>(tmp) = __ldg(reinterpret_cast<const uint4*>(s + col) + i);
-#pragma unroll
-                for (int j = 0; j < V; ++j) sc[i * V + j] = to_f32(tmp[j]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sc[i] = 0.f;
+        for (int j = 0; j < 4; ++j) {
+            const int c = col + 4 * t + j;
+            ST v;
+            if (c < limit) v = s[c];
+            else memset(&v, 0, sizeof v);
+            d[j] = v;
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sc[i] = col + i < limit ? to_f32(s[col + i]) : 0.f;
     }
 }
 
@@ -206,25 +209,27 @@ __device__ __forceinline__ void block_fma(float (&acc)[NT8][8][4], const uint2 (
     }
 }
 
-// One warp's blocks [b0, b1) of a staged chunk whose first row is row0.
-template <int NT8, typename ST, bool VEC>
-__device__ __forceinline__ void chunk_fma(float (&acc)[NT8][8][4], const Weight<ST>& W, int row0, int b0, int b1, int col,
-                                          int limit, const __half* xs, const float* bias, int g, int t) {
-    if (b0 >= b1) return;
-    uint2 w[2][8];
-    load_words<VEC>(w[0], W.q, W.row_bytes, row0 + b0 * kBlock + 8 * t, W.K, col, limit);
-    for (int b = b0; b < b1; ++b) {
-        uint2(&cur)[8] = w[0];
-        uint2(&nxt)[8] = w[1];
-        if (b + 1 < b1)
-            load_words<VEC>(nxt, W.q, W.row_bytes, row0 + (b + 1) * kBlock + 8 * t, W.K, col, limit);
-        float sc[16];
-        load_scales<ST, VEC>(sc, W.s + (long long)((row0 + b * kBlock) / W.group) * W.N, col, limit);
-        block_fma<NT8>(acc, cur, sc, xs + b * kBlock, bias + b * NT8 * 8, g, t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cur[i] = nxt[i];
+// The blocks a warp takes of a slice, in order: its quarter of every chunk.
+struct Blocks {
+    int row0, k1, quarter, b, b1;  // chunk's first row; block and end of the quarter
+
+    __device__ __forceinline__ void start(int row) {
+        row0 = row;
+        const int nblk = (min(kChunk, k1 - row0) + kBlock - 1) / kBlock;
+        b = nblk * quarter / kQuarters;
+        b1 = nblk * (quarter + 1) / kQuarters;
     }
-}
+    __device__ __forceinline__ bool done() const { return row0 >= k1; }
+    // to the next block that exists, chunk by chunk
+    __device__ __forceinline__ void settle() {
+        while (row0 < k1 && b >= b1) start(row0 + kChunk);
+    }
+    __device__ __forceinline__ void next() {
+        ++b;
+        settle();
+    }
+    __device__ __forceinline__ int row() const { return row0 + b * kBlock; }
+};
 
 // The f16 a value is staged as, and the power of two a bf16 row is
 // multiplied with (f16 rows: 1).
@@ -235,42 +240,105 @@ __device__ __forceinline__ float row_factor(float amax) {
     return __uint_as_float((uint32_t)(p + 127) << 23);
 }
 
-// Stage rows [row0, row0 + rows) of nt tokens (rows of x, ldx apart) as f16
-// times factor[token], zeros up to NT8 * 8 tokens and to a whole number of
-// blocks, and each block's bias.  All threads.
+// Stage rows [row0, row0 + rows) of nt tokens (rows of x, ldx apart) as f16,
+// zeros up to a whole number of blocks, and each block's bias.  bf16 rows are
+// multiplied by factor[token]; where the chunk is the whole slice (own), the
+// factor is found here.  A warp per token, 8 neighbouring values per lane.
+// Tokens past nt are left as they are: a token is a column of the products,
+// and what such columns hold reaches no other.
 template <int NT8, typename XT>
 __device__ __forceinline__ void stage_x(__half* xs, float* bias, const XT* x, long long ldx, int nt, int row0, int rows,
-                                        const float* factor) {
+                                        float* factor, bool own) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int nblk = (rows + kBlock - 1) / kBlock;
-    for (int i = warp; i < nblk * NT8 * 8; i += kThreads / 32) {
-        const int tok = i / nblk, b = i - tok * nblk;
-        const int r = b * kBlock + lane;
-        float v = 0.f;
-        if (tok < nt && r < rows) v = to_f32(x[tok * ldx + row0 + r]);
-        if constexpr (!std::is_same<XT, __half>::value) v *= tok < nt ? factor[tok] : 1.f;
-        const __half hv = __float2half_rn(v);
-        xs[tok * kXStride + r] = hv;
-        float s = __half2float(hv);
+    const int span = (rows + kBlock - 1) / kBlock * kBlock;
+    const bool vec = (ldx & 7) == 0;  // rows (and so 8 values) start on 16 bytes
+    constexpr int PASSES = kChunk / 256;
+    for (int tok = warp; tok < nt; tok += kWarps) {
+        const XT* xr = x + tok * ldx + row0;
+        float v[PASSES][8];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) bias[b * NT8 * 8 + tok] = s * -0x1p-21f;  // -8 2^-24
+        for (int p = 0; p < PASSES; ++p) {
+            const int r = p * 256 + lane * 8;
+            if (vec && r + 8 <= rows) {
+                XT tmp[8];
+                *reinterpret_cast<uint4*>(tmp) = *reinterpret_cast<const uint4*>(xr + r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[p][j] = to_f32(tmp[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[p][j] = r + j < rows ? to_f32(xr[r + j]) : 0.f;
+            }
+        }
+        float f = 1.f;
+        if constexpr (!std::is_same<XT, __half>::value) {
+            if (own) {
+                float m = 0.f;
+#pragma unroll
+                for (int p = 0; p < PASSES; ++p)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[p][j]));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                f = row_factor(m);
+                if (lane == 0) factor[tok] = f;
+            } else {
+                f = factor[tok];
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+            const int r = p * 256 + lane * 8;
+            __half2 h[4];
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[j] = __floats2half2_rn(v[p][2 * j] * f, v[p][2 * j + 1] * f);
+                const float2 b = __half22float2(h[j]);
+                s += b.x + b.y;
+            }
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            if (r < span) {
+                *reinterpret_cast<uint4*>(xs + tok * kXStride + r) = *reinterpret_cast<const uint4*>(h);
+                if ((lane & 3) == 0) bias[(r / kBlock) * NT8 * 8 + tok] = s * -0x1p-21f;  // -8 2^-24
+            }
+        }
     }
 }
 
 // The sums of this CTA's slice [k0, k1) of K, left in smem as [token][256
-// columns] fp32 (column c of half c / 128 is col0 + c or col1 + c - 128).
-// limit0 / limit1: the first column of each half that does not exist.
-// factor: smem, one per token, already set (bf16 tokens).
-template <int NT8, typename XT, typename ST, bool VEC>
+// columns] fp32 (column c of half c / 128 is col0 + c or col1 + c - 128) for
+// the nt tokens.  limit0 / limit1: the first column of each half that does
+// not exist.  factor: smem, one per token; set by the caller for slices of
+// more than one chunk of bf16 tokens.  before_x: called once the first
+// weight loads are on their way, before x is read.
+template <int NT8, typename XT, typename ST, bool VEC, typename F>
 __device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, int col0, int limit0, int col1, int limit1,
-                                           const XT* x, long long ldx, int nt, int k0, int k1, const float* factor) {
+                                           const XT* x, long long ldx, int nt, int k0, int k1, float* factor,
+                                           F&& before_x) {
+    using C = Cfg<NT8, ST>;
     __half* xs = reinterpret_cast<__half*>(smem);
-    float* bias = reinterpret_cast<float*>(smem + sizeof(__half) * NT8 * 8 * kXStride);
+    float* bias = reinterpret_cast<float*>(smem + C::X);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int half = warp & 1, quarter = warp >> 1;
     const int col = (half ? col1 : col0) + 16 * g, limit = half ? limit1 : limit0;
+    uint8_t* ring = smem + C::X + C::BIAS + warp * (C::STAGES * C::STAGE);
+    Blocks ahead{0, k1, quarter, 0, 0};  // the next block to load
+    ahead.start(k0);
+    ahead.settle();
+    int put = 0, get = 0;
+    auto issue = [&] {
+        if (!ahead.done()) {
+            issue_block<ST, VEC>(ring + put * C::STAGE, W, ahead.row(), col, limit, lane);
+            ahead.next();
+        }
+        op::cp_commit();  // (an empty group where nothing is left keeps the count)
+        put = put + 1 == C::STAGES ? 0 : put + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < C::STAGES - 1; ++i) issue();
+    before_x();
     float acc[NT8][8][4];
 #pragma unroll
     for (int n = 0; n < NT8; ++n)
@@ -278,15 +346,38 @@ __device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, i
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[n][i][c] = 0.f;
+    const bool own = k1 - k0 <= kChunk;
     for (int row0 = k0; row0 < k1; row0 += kChunk) {
-        const int rows = min(kChunk, k1 - row0);
-        const int nblk = (rows + kBlock - 1) / kBlock;
-        stage_x<NT8>(xs, bias, x, ldx, nt, row0, rows, factor);
+        if (row0 > k0) __syncthreads();  // the last chunk's x has been read
+        stage_x<NT8>(xs, bias, x, ldx, nt, row0, min(kChunk, k1 - row0), factor, own);
         __syncthreads();
-        const int b0 = nblk * quarter / kQuarters, b1 = nblk * (quarter + 1) / kQuarters;
-        chunk_fma<NT8, ST, VEC>(acc, W, row0, b0, b1, col, limit, xs, bias, g, t);
-        __syncthreads();
+        Blocks cur{0, k1, quarter, 0, 0};
+        cur.start(row0);
+        for (int b = cur.b; b < cur.b1; ++b) {
+            op::cp_wait<C::STAGES - 2>();
+            __syncwarp();  // the scales are other lanes' copies
+            const uint8_t* stage = ring + get * C::STAGE;
+            get = get + 1 == C::STAGES ? 0 : get + 1;
+            uint2 w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const uint2*>(stage)[i * 32 + lane];
+            float sc[16];
+            const ST* sp = reinterpret_cast<const ST*>(stage + C::WORDS) + g * 16;
+            constexpr int V = 16 / (int)sizeof(ST);
+#pragma unroll
+            for (int i = 0; i < 16 / V; ++i) {
+                ST tmp[V];
+                *reinterpret_cast<uint4*>(tmp) = reinterpret_cast<const uint4*>(sp)[i];
+#pragma unroll
+                for (int j = 0; j < V; ++j) sc[i * V + j] = to_f32(tmp[j]);
+            }
+            __syncwarp();  // every lane has read the stage that the next copies overwrite one turn on
+            issue();
+            block_fma<NT8>(acc, w, sc, xs + b * kBlock, bias + b * NT8 * 8, g, t);
+        }
     }
+    op::cp_wait<0>();
+    __syncthreads();
     // the quarters' sums, in their order
     float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
@@ -296,13 +387,15 @@ __device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, i
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int tok = n * 8 + 2 * t + (c & 1), f = half * 128 + 16 * g + tile_col(i) + (c & 2);
-                red[(quarter * NT8 * 8 + tok) * kCols + f] = acc[n][i][c] * ((i & 1) ? 0x1p20f : 0x1p24f);
+                if (tok < nt)
+                    red[(quarter * NT8 * 8 + tok) * kCols + f] = acc[n][i][c] * ((i & 1) ? 0x1p20f : 0x1p24f);
             }
     __syncthreads();
-    for (int i = threadIdx.x; i < NT8 * 8 * kCols; i += kThreads) {
+    for (int i = threadIdx.x; i < nt * kCols; i += kThreads) {
         float v = red[i];
 #pragma unroll
         for (int q = 1; q < kQuarters; ++q) v += red[q * NT8 * 8 * kCols + i];
+        if constexpr (!std::is_same<XT, __half>::value) v *= 1.0f / factor[i / kCols];
         red[i] = v;  // read and written by this thread alone
     }
 }
@@ -352,7 +445,7 @@ __host__ __forceinline__ int slices(long long tiles, int K, int sms) {
 // y [T, N] = x [T, K] W.  Grid: (column tiles, token tiles, slices), the
 // slices of a tile one cluster.
 template <int NT8, typename XT, typename ST, bool VEC>
-__global__ void __launch_bounds__(kThreads) int4_matvec_kernel(const XT* __restrict__ x, int T, Weight<ST> W,
+__global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const XT* __restrict__ x, int T, Weight<ST> W,
                                                                XT* __restrict__ y) {
     op::pdl_enter();
     extern __shared__ __align__(16) uint8_t mv_smem[];
@@ -362,15 +455,15 @@ __global__ void __launch_bounds__(kThreads) int4_matvec_kernel(const XT* __restr
     const int t0 = blockIdx.y * NT8 * 8, nt = min(NT8 * 8, T - t0);
     const int k0 = slice_row(W.K, slice, S), k1 = slice_row(W.K, slice + 1, S);
     const XT* xt = x + (long long)t0 * W.K;
-    if constexpr (!std::is_same<XT, __half>::value) {
-        slice_factors(factor, xt, W.K, nt, k0, k1);
-        __syncthreads();
-    }
-    slice_sums<NT8, XT, ST, VEC>(mv_smem, W, col0, W.N, col0 + 128, W.N, xt, W.K, nt, k0, k1, factor);
+    slice_sums<NT8, XT, ST, VEC>(mv_smem, W, col0, W.N, col0 + 128, W.N, xt, W.K, nt, k0, k1, factor, [&] {
+        if constexpr (!std::is_same<XT, __half>::value) {
+            if (k1 - k0 > kChunk) {  // several chunks share one factor
+                slice_factors(factor, xt, W.K, nt, k0, k1);
+                __syncthreads();
+            }
+        }
+    });
     float* red = reinterpret_cast<float*>(mv_smem);
-    if constexpr (!std::is_same<XT, __half>::value) {
-        for (int i = threadIdx.x; i < nt * kCols; i += kThreads) red[i] *= 1.0f / factor[i / kCols];
-    }
     if (S > 1) op::cluster_sync();
     else __syncthreads();
     const int items = nt * kCols;
@@ -445,7 +538,7 @@ __device__ __forceinline__ bool find_unit(const GroupTable* tab, int u, int& gro
 // gate/up tile is 128 hidden columns (gate in the first half, up in the
 // second), a down tile 256 columns.
 template <typename ST, bool GATE_UP>
-__global__ void __launch_bounds__(kThreads) experts_kernel(const GroupTable* tab, int num_experts, int group_rows,
+__global__ void __launch_bounds__(kThreads, 2) experts_kernel(const GroupTable* tab, int num_experts, int group_rows,
                                                            const __grid_constant__ Experts E, const Rows R) {
     op::pdl_enter();
     extern __shared__ __align__(16) uint8_t mv_smem[];
@@ -461,7 +554,7 @@ __global__ void __launch_bounds__(kThreads) experts_kernel(const GroupTable* tab
     const int k0 = slice_row(K, slice, S), k1 = slice_row(K, slice + 1, S);
     const Weight<ST> W{E.q[expert], static_cast<const ST*>(E.s[expert]), N / 2, N, K, group_rows};
     slice_sums<1, __half, ST, true>(mv_smem, W, col0, GATE_UP ? F : N, GATE_UP ? F + col0 : col0 + 128, N,
-                                    R.x[sh] + (long long)row0 * K, K, nt, k0, k1, nullptr);
+                                    R.x[sh] + (long long)row0 * K, K, nt, k0, k1, nullptr, [] {});
     const float* red = reinterpret_cast<const float*>(mv_smem);
     if (S > 1) op::cluster_sync();
     else __syncthreads();

@@ -470,7 +470,7 @@ struct ExpertWeights {
 template <typename ST, bool GATE_UP>
 void launch_experts_t(dim3 grid, cudaStream_t st, const GroupTable* tab, int E, int group, const mv::Experts& ptrs,
                       const mv::Rows& rows) {
-    constexpr size_t smem = mv::smem_bytes<1>();
+    constexpr size_t smem = mv::Cfg<1, ST>::SMEM;
     static std::atomic<uint64_t> attr_done{0};
     ensure_smem_attr(attr_done, mv::experts_kernel<ST, GATE_UP>, smem);
     launch_kc(mv::experts_kernel<ST, GATE_UP>, grid, dim3(mv::kThreads), smem, st, grid.z > 1 ? grid.z : 0u, tab, E,
