@@ -70,9 +70,9 @@ extern "C" l4moe_status l4moe_int4_matvec(int T, int K, int N, int group, const 
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return op_fail(L4MOE_ERR_CUDA, "l4moe_int4_matvec: no CUDA device");
-    // whole 8-byte words and aligned scale vectors when the rows are multiples of 16 columns
+    // 16-byte copies when every row starts on 16 bytes
     const Call c{T, K, N, group, sms, x, scales, static_cast<const uint8_t*>(w), y,
-                 static_cast<cudaStream_t>(stream), N % 16 == 0};
+                 static_cast<cudaStream_t>(stream), N % 32 == 0};
     const cudaError_t e =
         x_type == L4MOE_ELEM_BF16 ? launch_s<__nv_bfloat16>(c, s_type) : launch_s<__half>(c, s_type);
     if (e == cudaSuccess) return L4MOE_OK;

@@ -28,7 +28,7 @@
 // - The block's fp32 sum is multiplied by the group's scale and added to the
 //   column's total in fp32: the weights are never rounded to a product.
 // - Tokens are f16 in shared memory: f16 rows as they are, bf16 rows divided
-//   by a power of two that brings the largest of the slice to [2^14, 2^15)
+//   by a power of two that brings the largest of a quarter slice to [2^14, 2^15)
 //   (exact for values down to 2^-31 of it, others round at 2^-39 of it).
 //   A row with an infinity or a NaN gives NaN (inf times the bias).
 //
@@ -54,25 +54,26 @@ constexpr unsigned kErrF16Range = 1u << 4;  // DEV_ERR_F16_RANGE of the layer's 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCols = 256;       // columns of a CTA: two halves of 128
-constexpr int kQuarters = 4;     // warps of a half, each on a quarter of a chunk
+constexpr int kQuarters = 4;     // warps of a half, each on a quarter of the slice
 constexpr int kBlock = 32;       // rows of a block (scale groups are multiples of it)
-constexpr int kChunk = 1024;     // rows of x staged at a time
-constexpr int kXStride = kChunk + 32;  // halves; 64 bytes past a multiple of 128: the two
+constexpr int kPiece = 512;      // rows of x a quarter stages at a time
+constexpr int kXStride = kPiece + 32;  // halves; 64 bytes past a multiple of 128: the two
                                        // tokens of a quarter-warp's load use other banks
 
-// A warp's ring of weight blocks: 8 bytes per row and lane, each lane's own,
-// then the block's scales of the warp's 128 columns.
+// A warp's ring of weight blocks: 32 rows of 64 bytes (its 128 columns), then
+// their scales.  Each quarter has its part of x and of the block sums.
 template <int NT8, typename ST>
 struct Cfg {
-    static constexpr int WORDS = 8 * 32 * 8;
+    static constexpr int WORDS = kBlock * 64;
     static constexpr int STAGE = WORDS + 128 * (int)sizeof(ST);
     // two CTAs per SM want at most 113 KB each
     static constexpr int STAGES = (NT8 == 2 && sizeof(ST) == 4) ? 3 : 4;
-    static constexpr int X = (int)sizeof(__half) * NT8 * 8 * kXStride;
-    static constexpr int BIAS = (int)sizeof(float) * (kChunk / kBlock) * NT8 * 8;
+    static constexpr int X = (int)sizeof(__half) * NT8 * 8 * kXStride;       // of a quarter
+    static constexpr int BIAS = (int)sizeof(float) * (kPiece / kBlock) * NT8 * 8;
     static constexpr int RING = kWarps * STAGES * STAGE;
     static constexpr int RED = (int)sizeof(float) * kQuarters * NT8 * 8 * kCols;  // over all of it
-    static constexpr int SMEM = X + BIAS + RING > RED ? X + BIAS + RING : RED;
+    static constexpr int USED = kQuarters * (X + BIAS) + RING;
+    static constexpr int SMEM = USED > RED ? USED : RED;
 };
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
@@ -109,53 +110,89 @@ struct Weight {
     int K, group;
 };
 
-// Issue one block's loads into a stage: this lane's 8 rows of 8 bytes (16
-// columns), and its part of the scales of the warp's columns.  Rows past K
-// and columns past the limit are zeros.  VEC: asynchronous copies (rows of a
-// multiple of 16 columns); else plain loads, byte by byte.
+// Where a stage holds the 8 bytes of columns 16 g .. 16 g + 15 of row 8 t + i:
+// two rows to a 128-byte line, so that the 16 lanes of half a warp (4 values
+// of g, 4 of t) read 32 different banks.
+__device__ __forceinline__ int word_at(int i, int g, int t) {
+    return ((t >> 1) * 8 + i) * 128 + (t & 1) * 64 + ((((g >> 1) ^ (t & 2)) & 3) << 4) + (g & 1) * 8;
+}
+
+// A weight matrix's blocks as one lane loads them.  VEC (rows of a multiple
+// of 32 columns): asynchronous 16-byte copies, lane l 16 bytes of rows l / 4,
+// l / 4 + 8, ... and its four columns' scales; else plain loads of the lane's
+// own words, byte by byte.  What lies past K or past the columns' limit is
+// not loaded: x is zero there and such columns are not stored, and no nibble
+// is an infinity or a NaN.
 template <typename ST, bool VEC>
-__device__ __forceinline__ void issue_block(uint8_t* stage, const Weight<ST>& W, int row, int col, int limit, int lane) {
-    const int t = lane & 3, g = lane >> 2;
-    const int r0 = row + 8 * t;
-    const ST* s = W.s + (long long)(row / W.group) * W.N;
-    constexpr int WORDS = Cfg<1, ST>::WORDS;
-    constexpr int SB = 4 * (int)sizeof(ST);  // scale bytes of a lane: 4 columns
-    if constexpr (VEC) {
-        const bool in = col < limit;
-        const uint8_t* p = W.q + (in ? r0 * W.row_bytes + (col >> 1) : 0);
-        const uint32_t dst = op::smem_u32(stage) + lane * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool ok = in && r0 + i < W.K;
-            op::cp_async<8>(dst + i * 256, ok ? p + i * W.row_bytes : W.q, ok);
-        }
-        op::cp_async<SB>(op::smem_u32(stage) + WORDS + g * 16 * (int)sizeof(ST) + t * SB, in ? s + col + 4 * t : W.s, in);
-    } else {
-        const int nb = min(8, (limit - col + 1) >> 1);  // limit and col are even: whole bytes
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t lo = 0u, hi = 0u;
-            if (r0 + i < W.K) {
-                const uint8_t* p = W.q + (r0 + i) * W.row_bytes + (col >> 1);
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if (b < nb) lo |= (uint32_t)__ldg(p + b) << (8 * b);
-                    if (4 + b < nb) hi |= (uint32_t)__ldg(p + 4 + b) << (8 * b);
-                }
-            }
-            reinterpret_cast<uint2*>(stage)[i * 32 + lane] = make_uint2(lo, hi);
-        }
-        ST* d = reinterpret_cast<ST*>(stage + WORDS) + g * 16 + t * 4;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = col + 4 * t + j;
-            ST v;
-            if (c < limit) v = s[c];
-            else memset(&v, 0, sizeof v);
-            d[j] = v;
+struct Loader {
+    const uint8_t* q;     // VEC: this lane's 16 bytes of row 0; else the matrix
+    const ST* s;          // this lane's 4 scales of the current group (VEC), or of row 0's columns
+    long long row_bytes;
+    int N, K, group, col, limit;
+    int row, end;         // next block's row, end of the quarter
+    int left;             // rows until the next group
+
+    __device__ __forceinline__ void start(const Weight<ST>& W, int c0, int lim, int r0, int r1, int lane) {
+        row_bytes = W.row_bytes, N = W.N, K = W.K, group = W.group;
+        row = r0, end = r1, limit = lim;
+        const int grp = r0 / group;
+        left = group - (r0 - grp * group);
+        if constexpr (VEC) {
+            col = c0 + (lane & 3) * 32;
+            q = W.q + (long long)(r0 + (lane >> 2)) * row_bytes + (col >> 1);
+            s = W.s + (long long)grp * N + c0 + lane * 4;
+            limit = lim - c0;
+        } else {
+            col = c0 + 16 * (lane >> 2);
+            q = W.q;
+            s = W.s + (long long)grp * N;
         }
     }
-}
+    __device__ __forceinline__ void issue(uint8_t* stage, int lane) {
+        constexpr int WORDS = Cfg<1, ST>::WORDS;
+        if constexpr (VEC) {
+            const uint32_t base = op::smem_u32(stage);
+            if ((lane & 3) * 32 < limit) {
+                const uint32_t dst = base + (lane >> 2) * 128 + (lane & 3) * 16;
+                const uint8_t* p = q;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // t = i: line half i & 1, lines from (i / 2) 8, chunks swapped by i & 2
+                    if (row + i * 8 + (lane >> 2) < K)
+                        op::cp_async<16>((dst + (i >> 1) * 1024 + (i & 1) * 64) ^ ((i & 2) * 16), p);
+                    p += 8 * row_bytes;
+                }
+            }
+            if (lane * 4 < limit) op::cp_async<4 * (int)sizeof(ST)>(base + WORDS + lane * 4 * (int)sizeof(ST), s);
+            q += kBlock * row_bytes;
+        } else {
+            const int t = lane & 3, g = lane >> 2;
+            const int nb = min(8, (limit - col + 1) >> 1);  // limit and col are even: whole bytes
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t lo = 0u, hi = 0u;
+                if (row + 8 * t + i < K) {
+                    const uint8_t* p = q + (row + 8 * t + i) * row_bytes + (col >> 1);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        if (b < nb) lo |= (uint32_t)__ldg(p + b) << (8 * b);
+                        if (4 + b < nb) hi |= (uint32_t)__ldg(p + 4 + b) << (8 * b);
+                    }
+                }
+                *reinterpret_cast<uint2*>(stage + word_at(i, g, t)) = make_uint2(lo, hi);
+            }
+            ST* d = reinterpret_cast<ST*>(stage + WORDS) + g * 16 + t * 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (col + 4 * t + j < limit) d[j] = s[col + 4 * t + j];
+        }
+        row += kBlock;
+        left -= kBlock;
+        if (left == 0) {
+            left = group;
+            s += N;
+        }
+    }
+};
 
 // Column (of a thread's 16) that accumulator tile i holds in its first row
 // (c0, c1); its second row (c2, c3) is two columns on.  Odd tiles hold 16
@@ -209,28 +246,6 @@ __device__ __forceinline__ void block_fma(float (&acc)[NT8][8][4], const uint2 (
     }
 }
 
-// The blocks a warp takes of a slice, in order: its quarter of every chunk.
-struct Blocks {
-    int row0, k1, quarter, b, b1;  // chunk's first row; block and end of the quarter
-
-    __device__ __forceinline__ void start(int row) {
-        row0 = row;
-        const int nblk = (min(kChunk, k1 - row0) + kBlock - 1) / kBlock;
-        b = nblk * quarter / kQuarters;
-        b1 = nblk * (quarter + 1) / kQuarters;
-    }
-    __device__ __forceinline__ bool done() const { return row0 >= k1; }
-    // to the next block that exists, chunk by chunk
-    __device__ __forceinline__ void settle() {
-        while (row0 < k1 && b >= b1) start(row0 + kChunk);
-    }
-    __device__ __forceinline__ void next() {
-        ++b;
-        settle();
-    }
-    __device__ __forceinline__ int row() const { return row0 + b * kBlock; }
-};
-
 // The f16 a value is staged as, and the power of two a bf16 row is
 // multiplied with (f16 rows: 1).
 __device__ __forceinline__ float row_factor(float amax) {
@@ -242,18 +257,18 @@ __device__ __forceinline__ float row_factor(float amax) {
 
 // Stage rows [row0, row0 + rows) of nt tokens (rows of x, ldx apart) as f16,
 // zeros up to a whole number of blocks, and each block's bias.  bf16 rows are
-// multiplied by factor[token]; where the chunk is the whole slice (own), the
-// factor is found here.  A warp per token, 8 neighbouring values per lane.
-// Tokens past nt are left as they are: a token is a column of the products,
-// and what such columns hold reaches no other.
+// multiplied by factor[token]; where the piece is all of the quarter (own),
+// the factor is found here.  The quarter's two warps (half = 0, 1) take the
+// tokens in turn, 8 neighbouring values per lane.  Tokens past nt are left as
+// they are: a token is a column of the products, and what such a column holds
+// reaches no other.
 template <int NT8, typename XT>
 __device__ __forceinline__ void stage_x(__half* xs, float* bias, const XT* x, long long ldx, int nt, int row0, int rows,
-                                        float* factor, bool own) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+                                        float* factor, bool own, int half, int lane) {
     const int span = (rows + kBlock - 1) / kBlock * kBlock;
     const bool vec = (ldx & 7) == 0;  // rows (and so 8 values) start on 16 bytes
-    constexpr int PASSES = kChunk / 256;
-    for (int tok = warp; tok < nt; tok += kWarps) {
+    constexpr int PASSES = kPiece / 256;
+    for (int tok = half; tok < nt; tok += 2) {
         const XT* xr = x + tok * ldx + row0;
         float v[PASSES][8];
 #pragma unroll
@@ -306,33 +321,45 @@ __device__ __forceinline__ void stage_x(__half* xs, float* bias, const XT* x, lo
     }
 }
 
+// Each token's factor over rows [r0, r1) (bf16 tokens, more than one piece).
+template <typename XT>
+__device__ __forceinline__ void find_factors(float* factor, const XT* x, long long ldx, int nt, int r0, int r1, int half,
+                                             int lane) {
+    for (int tok = half; tok < nt; tok += 2) {
+        float m = 0.f;
+#pragma unroll 8
+        for (int k = r0 + lane; k < r1; k += 32) m = fmaxf(m, fabsf(to_f32(x[tok * ldx + k])));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) factor[tok] = row_factor(m);
+    }
+}
+
 // The sums of this CTA's slice [k0, k1) of K, left in smem as [token][256
 // columns] fp32 (column c of half c / 128 is col0 + c or col1 + c - 128) for
 // the nt tokens.  limit0 / limit1: the first column of each half that does
-// not exist.  factor: smem, one per token; set by the caller for slices of
-// more than one chunk of bf16 tokens.  before_x: called once the first
-// weight loads are on their way, before x is read.
+// not exist.  before_x: called once the first weight loads are on their way,
+// before x is read.
 template <int NT8, typename XT, typename ST, bool VEC, typename F>
 __device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, int col0, int limit0, int col1, int limit1,
-                                           const XT* x, long long ldx, int nt, int k0, int k1, float* factor,
-                                           F&& before_x) {
+                                           const XT* x, long long ldx, int nt, int k0, int k1, F&& before_x) {
     using C = Cfg<NT8, ST>;
-    __half* xs = reinterpret_cast<__half*>(smem);
-    float* bias = reinterpret_cast<float*>(smem + C::X);
+    constexpr bool BF = !std::is_same<XT, __half>::value;
+    __shared__ float s_factor[kQuarters][NT8 * 8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int half = warp & 1, quarter = warp >> 1;
-    const int col = (half ? col1 : col0) + 16 * g, limit = half ? limit1 : limit0;
-    uint8_t* ring = smem + C::X + C::BIAS + warp * (C::STAGES * C::STAGE);
-    Blocks ahead{0, k1, quarter, 0, 0};  // the next block to load
-    ahead.start(k0);
-    ahead.settle();
+    __half* xs = reinterpret_cast<__half*>(smem + quarter * (C::X + C::BIAS));
+    float* bias = reinterpret_cast<float*>(smem + quarter * (C::X + C::BIAS) + C::X);
+    uint8_t* ring = smem + kQuarters * (C::X + C::BIAS) + warp * (C::STAGES * C::STAGE);
+    const int nblk = (k1 - k0 + kBlock - 1) / kBlock;
+    const int r0 = k0 + nblk * quarter / kQuarters * kBlock;
+    const int r1 = min(k1, k0 + nblk * (quarter + 1) / kQuarters * kBlock);
+    Loader<ST, VEC> ld;
+    ld.start(W, half ? col1 : col0, half ? limit1 : limit0, r0, r1, lane);
     int put = 0, get = 0;
     auto issue = [&] {
-        if (!ahead.done()) {
-            issue_block<ST, VEC>(ring + put * C::STAGE, W, ahead.row(), col, limit, lane);
-            ahead.next();
-        }
+        if (ld.row < r1) ld.issue(ring + put * C::STAGE, lane);
         op::cp_commit();  // (an empty group where nothing is left keeps the count)
         put = put + 1 == C::STAGES ? 0 : put + 1;
     };
@@ -346,21 +373,23 @@ __device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, i
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[n][i][c] = 0.f;
-    const bool own = k1 - k0 <= kChunk;
-    for (int row0 = k0; row0 < k1; row0 += kChunk) {
-        if (row0 > k0) __syncthreads();  // the last chunk's x has been read
-        stage_x<NT8>(xs, bias, x, ldx, nt, row0, min(kChunk, k1 - row0), factor, own);
-        __syncthreads();
-        Blocks cur{0, k1, quarter, 0, 0};
-        cur.start(row0);
-        for (int b = cur.b; b < cur.b1; ++b) {
+    const bool own = r1 - r0 <= kPiece;
+    if (BF && !own) find_factors(s_factor[quarter], x, ldx, nt, r0, r1, half, lane);  // (a token's warp reads it back)
+    const int words = word_at(0, g, t);
+    for (int row0 = r0; row0 < r1; row0 += kPiece) {
+        const int rows = min(kPiece, r1 - row0);
+        if (row0 > r0) op::pair_sync(1 + quarter);  // the last piece of x has been read
+        else __syncwarp();
+        stage_x<NT8>(xs, bias, x, ldx, nt, row0, rows, s_factor[quarter], own, half, lane);
+        op::pair_sync(1 + quarter);
+        for (int b = 0; b * kBlock < rows; ++b) {
             op::cp_wait<C::STAGES - 2>();
-            __syncwarp();  // the scales are other lanes' copies
+            __syncwarp();  // the copies are other lanes'
             const uint8_t* stage = ring + get * C::STAGE;
             get = get + 1 == C::STAGES ? 0 : get + 1;
             uint2 w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const uint2*>(stage)[i * 32 + lane];
+            for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint2*>(stage + words + i * 128);
             float sc[16];
             const ST* sp = reinterpret_cast<const ST*>(stage + C::WORDS) + g * 16;
             constexpr int V = 16 / (int)sizeof(ST);
@@ -371,7 +400,8 @@ __device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, i
 #pragma unroll
                 for (int j = 0; j < V; ++j) sc[i * V + j] = to_f32(tmp[j]);
             }
-            __syncwarp();  // every lane has read the stage that the next copies overwrite one turn on
+            // (the copies issued here go to the stage read one turn ago: every
+            // lane has passed this turn's __syncwarp since)
             issue();
             block_fma<NT8>(acc, w, sc, xs + b * kBlock, bias + b * NT8 * 8, g, t);
         }
@@ -383,19 +413,20 @@ __device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, i
 #pragma unroll
     for (int n = 0; n < NT8; ++n)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int c = 0; c < 4; ++c) {
+            const int tok = n * 8 + 2 * t + (c & 1);
+            if (tok < nt) {
+                const float f = BF && r0 < r1 ? 1.0f / s_factor[quarter][tok] : 1.0f;
+                float* o = red + (quarter * NT8 * 8 + tok) * kCols + half * 128 + 16 * g + (c & 2);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int tok = n * 8 + 2 * t + (c & 1), f = half * 128 + 16 * g + tile_col(i) + (c & 2);
-                if (tok < nt)
-                    red[(quarter * NT8 * 8 + tok) * kCols + f] = acc[n][i][c] * ((i & 1) ? 0x1p20f : 0x1p24f);
+                for (int i = 0; i < 8; ++i) o[tile_col(i)] = acc[n][i][c] * ((i & 1) ? 0x1p20f : 0x1p24f) * f;
             }
+        }
     __syncthreads();
     for (int i = threadIdx.x; i < nt * kCols; i += kThreads) {
         float v = red[i];
 #pragma unroll
         for (int q = 1; q < kQuarters; ++q) v += red[q * NT8 * 8 * kCols + i];
-        if constexpr (!std::is_same<XT, __half>::value) v *= 1.0f / factor[i / kCols];
         red[i] = v;  // read and written by this thread alone
     }
 }
@@ -407,21 +438,6 @@ __device__ __forceinline__ float cluster_total(const float* red, int i, int slic
     float v = 0.f;
     for (int r = 0; r < slices; ++r) v += op::ld_cluster_f32(op::mapa(at, (uint32_t)r));
     return v;
-}
-
-// Each token's largest magnitude over a slice -> factor (bf16 tokens).
-template <typename XT>
-__device__ __forceinline__ void slice_factors(float* factor, const XT* x, long long ldx, int nt, int k0, int k1) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int tok = warp; tok < nt; tok += kThreads / 32) {
-        float m = 0.f;
-        for (int k = k0 + lane; k < k1; k += 32) {
-            m = fmaxf(m, fabsf(to_f32(x[tok * ldx + k])));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) factor[tok] = row_factor(m);
-    }
 }
 
 // Rows [k0, k1) of slice r of S: whole blocks, as even as they come.
@@ -448,21 +464,13 @@ template <int NT8, typename XT, typename ST, bool VEC>
 __global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const XT* __restrict__ x, int T, Weight<ST> W,
                                                                XT* __restrict__ y) {
     op::pdl_enter();
-    extern __shared__ __align__(16) uint8_t mv_smem[];
-    __shared__ float factor[NT8 * 8];
+    extern __shared__ __align__(128) uint8_t mv_smem[];
     const int S = gridDim.z, slice = blockIdx.z;
     const int col0 = blockIdx.x * kCols;
     const int t0 = blockIdx.y * NT8 * 8, nt = min(NT8 * 8, T - t0);
     const int k0 = slice_row(W.K, slice, S), k1 = slice_row(W.K, slice + 1, S);
     const XT* xt = x + (long long)t0 * W.K;
-    slice_sums<NT8, XT, ST, VEC>(mv_smem, W, col0, W.N, col0 + 128, W.N, xt, W.K, nt, k0, k1, factor, [&] {
-        if constexpr (!std::is_same<XT, __half>::value) {
-            if (k1 - k0 > kChunk) {  // several chunks share one factor
-                slice_factors(factor, xt, W.K, nt, k0, k1);
-                __syncthreads();
-            }
-        }
-    });
+    slice_sums<NT8, XT, ST, VEC>(mv_smem, W, col0, W.N, col0 + 128, W.N, xt, W.K, nt, k0, k1, [] {});
     float* red = reinterpret_cast<float*>(mv_smem);
     if (S > 1) op::cluster_sync();
     else __syncthreads();
@@ -541,7 +549,7 @@ template <typename ST, bool GATE_UP>
 __global__ void __launch_bounds__(kThreads, 2) experts_kernel(const GroupTable* tab, int num_experts, int group_rows,
                                                            const __grid_constant__ Experts E, const Rows R) {
     op::pdl_enter();
-    extern __shared__ __align__(16) uint8_t mv_smem[];
+    extern __shared__ __align__(128) uint8_t mv_smem[];
     int grp, row;
     if (!find_unit(tab, blockIdx.y, grp, row)) return;
     const int expert = tab->expert[grp], sh = expert == num_experts ? 1 : 0;
@@ -554,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(const GroupTable* 
     const int k0 = slice_row(K, slice, S), k1 = slice_row(K, slice + 1, S);
     const Weight<ST> W{E.q[expert], static_cast<const ST*>(E.s[expert]), N / 2, N, K, group_rows};
     slice_sums<1, __half, ST, true>(mv_smem, W, col0, GATE_UP ? F : N, GATE_UP ? F + col0 : col0 + 128, N,
-                                    R.x[sh] + (long long)row0 * K, K, nt, k0, k1, nullptr, [] {});
+                                    R.x[sh] + (long long)row0 * K, K, nt, k0, k1, [] {});
     const float* red = reinterpret_cast<const float*>(mv_smem);
     if (S > 1) op::cluster_sync();
     else __syncthreads();
