@@ -66,8 +66,10 @@ template <int NT8, typename ST>
 struct Cfg {
     static constexpr int WORDS = kBlock * 64;
     static constexpr int STAGE = WORDS + 128 * (int)sizeof(ST);
-    // two CTAs per SM want at most 113 KB each
-    static constexpr int STAGES = (NT8 == 2 && sizeof(ST) == 4) ? 3 : 4;
+    // up to 8 tokens two CTAs share an SM (128 registers a thread, 113 KB
+    // each); for 16 tokens the sums alone take 64, and one CTA has it
+    static constexpr int PER_SM = NT8 == 1 ? 2 : 1;
+    static constexpr int STAGES = NT8 == 1 ? 4 : 6;
     static constexpr int X = (int)sizeof(__half) * NT8 * 8 * kXStride;       // of a quarter
     static constexpr int BIAS = (int)sizeof(float) * (kPiece / kBlock) * NT8 * 8;
     static constexpr int RING = kWarps * STAGES * STAGE;
@@ -131,12 +133,14 @@ struct Loader {
     int N, K, group, col, limit;
     int row, end;         // next block's row, end of the quarter
     int left;             // rows until the next group
+    bool fresh;           // the next block is this warp's first of its group
 
     __device__ __forceinline__ void start(const Weight<ST>& W, int c0, int lim, int r0, int r1, int lane) {
         row_bytes = W.row_bytes, N = W.N, K = W.K, group = W.group;
         row = r0, end = r1, limit = lim;
         const int grp = r0 / group;
         left = group - (r0 - grp * group);
+        fresh = true;
         if constexpr (VEC) {
             col = c0 + (lane & 3) * 32;
             q = W.q + (long long)(r0 + (lane >> 2)) * row_bytes + (col >> 1);
@@ -155,14 +159,16 @@ struct Loader {
             if ((lane & 3) * 32 < limit) {
                 const uint32_t dst = base + (lane >> 2) * 128 + (lane & 3) * 16;
                 const uint8_t* p = q;
+                const bool whole = row + kBlock <= K;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {  // t = i: line half i & 1, lines from (i / 2) 8, chunks swapped by i & 2
-                    if (row + i * 8 + (lane >> 2) < K)
+                    if (whole || row + i * 8 + (lane >> 2) < K)
                         op::cp_async<16>((dst + (i >> 1) * 1024 + (i & 1) * 64) ^ ((i & 2) * 16), p);
                     p += 8 * row_bytes;
                 }
             }
-            if (lane * 4 < limit) op::cp_async<4 * (int)sizeof(ST)>(base + WORDS + lane * 4 * (int)sizeof(ST), s);
+            if (fresh && lane * 4 < limit)
+                op::cp_async<4 * (int)sizeof(ST)>(base + WORDS + lane * 4 * (int)sizeof(ST), s);
             q += kBlock * row_bytes;
         } else {
             const int t = lane & 3, g = lane >> 2;
@@ -183,11 +189,12 @@ struct Loader {
             ST* d = reinterpret_cast<ST*>(stage + WORDS) + g * 16 + t * 4;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (col + 4 * t + j < limit) d[j] = s[col + 4 * t + j];
+                if (fresh && col + 4 * t + j < limit) d[j] = s[col + 4 * t + j];
         }
         row += kBlock;
         left -= kBlock;
-        if (left == 0) {
+        fresh = left == 0;
+        if (fresh) {
             left = group;
             s += N;
         }
@@ -268,6 +275,7 @@ __device__ __forceinline__ void stage_x(__half* xs, float* bias, const XT* x, lo
     const int span = (rows + kBlock - 1) / kBlock * kBlock;
     const bool vec = (ldx & 7) == 0;  // rows (and so 8 values) start on 16 bytes
     constexpr int PASSES = kPiece / 256;
+#pragma unroll 2
     for (int tok = half; tok < nt; tok += 2) {
         const XT* xr = x + tok * ldx + row0;
         float v[PASSES][8];
@@ -376,6 +384,8 @@ __device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, i
     const bool own = r1 - r0 <= kPiece;
     if (BF && !own) find_factors(s_factor[quarter], x, ldx, nt, r0, r1, half, lane);  // (a token's warp reads it back)
     const int words = word_at(0, g, t);
+    float sc[16];
+    int left = 0;  // rows that the scales at hand still cover
     for (int row0 = r0; row0 < r1; row0 += kPiece) {
         const int rows = min(kPiece, r1 - row0);
         if (row0 > r0) op::pair_sync(1 + quarter);  // the last piece of x has been read
@@ -390,16 +400,19 @@ __device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, i
             uint2 w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint2*>(stage + words + i * 128);
-            float sc[16];
-            const ST* sp = reinterpret_cast<const ST*>(stage + C::WORDS) + g * 16;
-            constexpr int V = 16 / (int)sizeof(ST);
+            if (left == 0) {  // a group's first block brings its scales
+                const ST* sp = reinterpret_cast<const ST*>(stage + C::WORDS) + g * 16;
+                constexpr int V = 16 / (int)sizeof(ST);
 #pragma unroll
-            for (int i = 0; i < 16 / V; ++i) {
-                ST tmp[V];
-                *reinterpret_cast<uint4*>(tmp) = reinterpret_cast<const uint4*>(sp)[i];
+                for (int i = 0; i < 16 / V; ++i) {
+                    ST tmp[V];
+                    *reinterpret_cast<uint4*>(tmp) = reinterpret_cast<const uint4*>(sp)[i];
 #pragma unroll
-                for (int j = 0; j < V; ++j) sc[i * V + j] = to_f32(tmp[j]);
+                    for (int j = 0; j < V; ++j) sc[i * V + j] = to_f32(tmp[j]);
+                }
+                left = W.group - (row0 + b * kBlock) % W.group;
             }
+            left -= kBlock;
             // (the copies issued here go to the stage read one turn ago: every
             // lane has passed this turn's __syncwarp since)
             issue();
@@ -440,20 +453,19 @@ __device__ __forceinline__ float cluster_total(const float* red, int i, int slic
     return v;
 }
 
-// Rows [k0, k1) of slice r of S: whole blocks, as even as they come.
-__host__ __device__ __forceinline__ int slice_row(int K, int r, int S) {
-    const int blocks = (K + kBlock - 1) / kBlock;
-    const int k = (int)((long long)blocks * r / S) * kBlock;
+// First row of slice r of 2^lg: whole blocks, as even as they come.
+__host__ __device__ __forceinline__ int slice_row(int K, int r, int lg) {
+    const int blocks = (K + kBlock - 1) / kBlock;  // K <= 2^30: blocks * 8 fits
+    const int k = ((blocks * r) >> lg) * kBlock;
     return k < K ? k : K;
 }
 
-// Slices of K for a launch of `tiles` tiles: enough CTAs for two on every SM
-// (what their registers and shared memory allow), a block at least for each
-// quarter, at most a portable cluster.
+// Slices of K (a power of two) for a launch of `tiles` tiles: a CTA for every
+// SM, a block at least for each quarter, at most a portable cluster.
 __host__ __forceinline__ int slices(long long tiles, int K, int sms) {
     const int blocks = (K + kBlock - 1) / kBlock;
     int S = 1;
-    while (S < 8 && tiles * S < 2LL * sms && blocks >= 2 * S * kQuarters) S *= 2;
+    while (S < 8 && tiles * S < sms && blocks >= 2 * S * kQuarters) S *= 2;
     return S;
 }
 
@@ -461,21 +473,21 @@ __host__ __forceinline__ int slices(long long tiles, int K, int sms) {
 // y [T, N] = x [T, K] W.  Grid: (column tiles, token tiles, slices), the
 // slices of a tile one cluster.
 template <int NT8, typename XT, typename ST, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) int4_matvec_kernel(const XT* __restrict__ x, int T, Weight<ST> W,
+__global__ void __launch_bounds__(kThreads, Cfg<NT8, ST>::PER_SM) int4_matvec_kernel(const XT* __restrict__ x, int T, Weight<ST> W,
                                                                XT* __restrict__ y) {
     op::pdl_enter();
     extern __shared__ __align__(128) uint8_t mv_smem[];
-    const int S = gridDim.z, slice = blockIdx.z;
+    const int S = gridDim.z, slice = blockIdx.z, lg = __ffs(S) - 1;
     const int col0 = blockIdx.x * kCols;
     const int t0 = blockIdx.y * NT8 * 8, nt = min(NT8 * 8, T - t0);
-    const int k0 = slice_row(W.K, slice, S), k1 = slice_row(W.K, slice + 1, S);
+    const int k0 = slice_row(W.K, slice, lg), k1 = slice_row(W.K, slice + 1, lg);
     const XT* xt = x + (long long)t0 * W.K;
     slice_sums<NT8, XT, ST, VEC>(mv_smem, W, col0, W.N, col0 + 128, W.N, xt, W.K, nt, k0, k1, [] {});
     float* red = reinterpret_cast<float*>(mv_smem);
     if (S > 1) op::cluster_sync();
     else __syncthreads();
     const int items = nt * kCols;
-    const int i0 = (int)((long long)items * slice / S), i1 = (int)((long long)items * (slice + 1) / S);
+    const int i0 = (items >> lg) * slice, i1 = i0 + (items >> lg);  // items is a multiple of 8
     for (int i = i0 + threadIdx.x; i < i1; i += kThreads) {
         const int tok = i / kCols, n = col0 + i % kCols;
         if (n >= W.N) continue;
@@ -558,8 +570,8 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(const GroupTable* 
     const int F = N / 2;
     const int col0 = blockIdx.x * (GATE_UP ? 128 : kCols);
     if (col0 >= (GATE_UP ? F : N)) return;
-    const int S = gridDim.z, slice = blockIdx.z;
-    const int k0 = slice_row(K, slice, S), k1 = slice_row(K, slice + 1, S);
+    const int S = gridDim.z, slice = blockIdx.z, lg = __ffs(S) - 1;
+    const int k0 = slice_row(K, slice, lg), k1 = slice_row(K, slice + 1, lg);
     const Weight<ST> W{E.q[expert], static_cast<const ST*>(E.s[expert]), N / 2, N, K, group_rows};
     slice_sums<1, __half, ST, true>(mv_smem, W, col0, GATE_UP ? F : N, GATE_UP ? F + col0 : col0 + 128, N,
                                     R.x[sh] + (long long)row0 * K, K, nt, k0, k1, [] {});
@@ -567,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(const GroupTable* 
     if (S > 1) op::cluster_sync();
     else __syncthreads();
     const int width = GATE_UP ? 128 : kCols, items = nt * width;
-    const int i0 = (int)((long long)items * slice / S), i1 = (int)((long long)items * (slice + 1) / S);
+    const int i0 = (items >> lg) * slice, i1 = i0 + (items >> lg);  // items is a multiple of 8
     for (int i = i0 + threadIdx.x; i < i1; i += kThreads) {
         const int tok = i / width, c = i % width;
         if (GATE_UP) {
