@@ -26,7 +26,7 @@ cudaError_t launch(const Call& c) {
     static std::atomic<uint64_t> attr_done{0};
     ensure_smem_attr(attr_done, mv::int4_matvec_kernel<NT8, XT, ST, VEC>, smem);
     const int tiles = (c.N + mv::kCols - 1) / mv::kCols, tt = (c.T + NT8 * 8 - 1) / (NT8 * 8);
-    const int S = mv::slices((long long)tiles * tt, c.K, c.sms);
+    const int S = mv::slices((long long)tiles * tt, c.K, c.sms, mv::Cfg<NT8, ST>::PER_SM);
     const mv::Weight<ST> W{c.w, static_cast<const ST*>(c.s), c.N / 2, c.N, c.K, c.group};
     launch_kc(mv::int4_matvec_kernel<NT8, XT, ST, VEC>, dim3(tiles, tt, S), dim3(mv::kThreads), smem, c.st,
               S > 1 ? (unsigned)S : 0u, static_cast<const XT*>(c.x), c.T, W, static_cast<XT*>(c.y));

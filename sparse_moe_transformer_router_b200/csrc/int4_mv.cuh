@@ -8,23 +8,24 @@
 // operator and by the layer's experts when their scales are grouped.
 //
 // With a handful of tokens the weight's bytes bound the product (one multiply
-// per half byte and token), so every weight byte goes from global memory
-// straight to the registers of the one warp that needs it, and the work per
-// weight is kept small enough to run beside the loads:
+// per half byte and token), so every weight byte is read once, by the one
+// warp that needs it, and the work per weight is kept small enough to run
+// beside the loads:
 //
 // - mma.sync.m16n8k16 (f16 in, fp32 sums): weights as the 16-row operand, up
 //   to 8 tokens as the 8 columns.  tcgen05 would take its weight operand from
 //   shared memory, a round trip for widened weights that nothing is gained
 //   from at 8 columns.
-// - A thread holds 16 neighbouring columns of 8 neighbouring rows (an 8-byte
-//   load per row, 64 bytes of a row per warp).  The operand wants pairs along
-//   K, so two rows' words are interleaved by one byte permutation per four
-//   columns, and each pair of nibbles is then one AND (with the sign bit
-//   flipped) away: u = q + 8 in [0, 15] left where it lies in the f16's low
-//   bits is the subnormal u 2^-24 (or 16 u 2^-24 one nibble up), exact in the
-//   tensor core.  No conversion instruction, 0.75 per weight in all.
-// - The bias 8 leaves through the sum's start value: each 32-row block starts
-//   at -8 sum(x) (2^-24), from the tokens' block sums kept beside them.
+// - A warp takes blocks of 32 rows by 128 columns through a ring of its own
+//   in shared memory, filled by asynchronous 16-byte copies.  The operand
+//   wants pairs along K: a transposing matrix load of 16-bit units, four
+//   columns each, returns two rows' units in one register.  Each pair of
+//   nibbles is then one AND (with the sign bit flipped) away: u = q + 8 in
+//   [0, 15] left where it lies in the f16's low bits is the subnormal u 2^-24
+//   (or 16 u 2^-24 one nibble up), exact in the tensor core.  No conversion
+//   instruction, 0.625 per weight in all.
+// - The bias 8 leaves as -8 sum(x) (2^-24) times the group's scale, from the
+//   tokens' block sums kept beside them, once for each run of a group's blocks.
 // - The block's fp32 sum is multiplied by the group's scale and added to the
 //   column's total in fp32: the weights are never rounded to a product.
 // - Tokens are f16 in shared memory: f16 rows as they are, bf16 rows divided
@@ -32,10 +33,9 @@
 //   (exact for values down to 2^-31 of it, others round at 2^-39 of it).
 //   A row with an infinity or a NaN gives NaN (inf times the bias).
 //
-// A CTA takes 256 columns (two groups of 128) and a slice of K, four warps of
-// each column half on a quarter of the slice; the quarters are added through
-// shared memory and the slices of a cluster through distributed shared
-// memory, always in the same order.
+// A CTA of four warps takes 128 columns and a slice of K, each warp a quarter
+// of the slice; the quarters are added through shared memory and the slices
+// of a cluster through distributed shared memory, always in the same order.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -51,42 +51,46 @@ namespace mv {
 
 constexpr unsigned kErrF16Range = 1u << 4;  // DEV_ERR_F16_RANGE of the layer's error word
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kCols = 256;       // columns of a CTA: two halves of 128
-constexpr int kQuarters = 4;     // warps of a half, each on a quarter of the slice
+constexpr int kWarps = 4;        // of a CTA, each on a quarter of the CTA's slice of K
+constexpr int kThreads = 32 * kWarps;
+constexpr int kCols = 128;       // columns of a CTA: two halves of 64
+constexpr int kHalf = kCols / 2;
 constexpr int kBlock = 32;       // rows of a block (scale groups are multiples of it)
-constexpr int kPiece = 512;      // rows of x a quarter stages at a time
-constexpr int kXStride = kPiece + 32;  // halves; 64 bytes past a multiple of 128: the two
-                                       // tokens of a quarter-warp's load use other banks
 
-// A warp's ring of weight blocks: 32 rows of 64 bytes (its 128 columns), then
-// their scales.  Each quarter has its part of x and of the block sums.
+// A warp's shared memory: its part of x (f16) with the block sums, and a ring
+// of weight blocks (32 rows of 64 bytes, then the scales of the columns).
 template <int NT8, typename ST>
 struct Cfg {
     static constexpr int WORDS = kBlock * 64;
-    static constexpr int STAGE = WORDS + 128 * (int)sizeof(ST);
-    // up to 8 tokens two CTAs share an SM (128 registers a thread, 113 KB
-    // each); for 16 tokens the sums alone take 64, and one CTA has it
-    static constexpr int PER_SM = NT8 == 1 ? 2 : 1;
-    static constexpr int STAGES = NT8 == 1 ? 4 : 6;
-    static constexpr int X = (int)sizeof(__half) * NT8 * 8 * kXStride;       // of a quarter
-    static constexpr int BIAS = (int)sizeof(float) * (kPiece / kBlock) * NT8 * 8;
-    static constexpr int RING = kWarps * STAGES * STAGE;
-    static constexpr int RED = (int)sizeof(float) * kQuarters * NT8 * 8 * kCols;  // over all of it
-    static constexpr int USED = kQuarters * (X + BIAS) + RING;
+    static constexpr int STAGE = WORDS + kCols * (int)sizeof(ST);
+    static constexpr int STAGES = 4;
+    static constexpr int RING = STAGES * STAGE;
+    static constexpr int X = NT8 * 4864;  // 256 rows of NT8 * 8 tokens, more of fewer (piece_rows)
+    // CTAs that share an SM: the registers' limit (up to 8 tokens 128 a
+    // thread, 16 tokens 168)
+    static constexpr int PER_SM = NT8 == 1 ? 4 : 3;
+    static constexpr int RED = (int)sizeof(float) * kWarps * NT8 * 8 * kCols;  // over all of it
+    static constexpr int USED = kWarps * (X + RING);
     static constexpr int SMEM = USED > RED ? USED : RED;
 };
+
+// Rows of x that a warp stages at a time: as many (a multiple of 128) as
+// nt token rows, 64 bytes apart in the banks, and their block sums (of whole
+// pairs of tokens) leave room for.
+__host__ __device__ __forceinline__ int piece_rows(int nt, int bytes) {
+    const int pair = (nt + 1) & ~1;
+    return (bytes - 64 * nt) / (256 * nt + 16 * pair) * 128;
+}
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                        uint32_t b0, uint32_t b1, float c0, float c1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+                                        uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_f16_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                             uint32_t b0, uint32_t b1) {
@@ -112,121 +116,121 @@ struct Weight {
     int K, group;
 };
 
-// Where a stage holds the 8 bytes of columns 16 g .. 16 g + 15 of row 8 t + i:
-// two rows to a 128-byte line, so that the 16 lanes of half a warp (4 values
-// of g, 4 of t) read 32 different banks.
-__device__ __forceinline__ int word_at(int i, int g, int t) {
-    return ((t >> 1) * 8 + i) * 128 + (t & 1) * 64 + ((((g >> 1) ^ (t & 2)) & 3) << 4) + (g & 1) * 8;
-}
+// Where a stage holds the 16 bytes of columns 32 c .. 32 c + 31 of row r: the
+// eight rows of a matrix load lie in different banks.
+__device__ __forceinline__ constexpr int chunk_at(int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); }
+
+// The 128 columns of a CTA: two runs of 64, each with the first column that
+// does not exist.
+struct Columns {
+    int col0, col1, limit0, limit1;
+    __device__ __forceinline__ int first(int second) const { return second ? col1 : col0; }
+    __device__ __forceinline__ int end(int second) const { return second ? limit1 : limit0; }
+};
 
 // A weight matrix's blocks as one lane loads them.  VEC (rows of a multiple
 // of 32 columns): asynchronous 16-byte copies, lane l 16 bytes of rows l / 4,
-// l / 4 + 8, ... and its four columns' scales; else plain loads of the lane's
-// own words, byte by byte.  What lies past K or past the columns' limit is
-// not loaded: x is zero there and such columns are not stored, and no nibble
-// is an infinity or a NaN.
+// l / 4 + 8, ... and its four columns' scales; else plain loads, byte by
+// byte.  What lies past K or past the columns' limit is not loaded: x is zero
+// there and such columns are not stored, and no nibble is an infinity or a
+// NaN.
 template <typename ST, bool VEC>
 struct Loader {
-    const uint8_t* q;     // VEC: this lane's 16 bytes of row 0; else the matrix
-    const ST* s;          // this lane's 4 scales of the current group (VEC), or of row 0's columns
+    const uint8_t* q;     // VEC: this lane's 16 bytes of its first row; else this lane's row
+    const ST* s;          // VEC: this lane's 4 scales of the next block; else the row of scales
     long long row_bytes;
-    int N, K, group, col, limit;
-    int row, end;         // next block's row, end of the quarter
+    int N, group;
     int left;             // rows until the next group
-    bool fresh;           // the next block is this warp's first of its group
+    int rows;             // rows of K left from the next block on
+    bool in, in_s;        // VEC: this lane's columns exist
 
-    __device__ __forceinline__ void start(const Weight<ST>& W, int c0, int lim, int r0, int r1, int lane) {
-        row_bytes = W.row_bytes, N = W.N, K = W.K, group = W.group;
-        row = r0, end = r1, limit = lim;
-        const int grp = r0 / group;
-        left = group - (r0 - grp * group);
-        fresh = true;
+    __device__ __forceinline__ void start(const Weight<ST>& W, const Columns& C, int row, int lane) {
+        row_bytes = W.row_bytes, N = W.N, group = W.group;
+        const int grp = row / group;
+        left = 0;
+        first = group - (row - grp * group);
+        rows = W.K - row;
+        s = W.s + (long long)grp * N;
         if constexpr (VEC) {
-            col = c0 + (lane & 3) * 32;
-            q = W.q + (long long)(r0 + (lane >> 2)) * row_bytes + (col >> 1);
-            s = W.s + (long long)grp * N + c0 + lane * 4;
-            limit = lim - c0;
+            const int col = C.first(lane & 2) + (lane & 1) * 32;
+            in = col < C.end(lane & 2);
+            q = W.q + (long long)(row + (lane >> 2)) * row_bytes + (col >> 1);
+            const int cs = C.first(lane & 16) + (lane & 15) * 4;
+            in_s = cs < C.end(lane & 16);
+            s += cs;
         } else {
-            col = c0 + 16 * (lane >> 2);
-            q = W.q;
-            s = W.s + (long long)grp * N;
+            q = W.q + (long long)(row + lane) * row_bytes;
         }
     }
-    __device__ __forceinline__ void issue(uint8_t* stage, int lane) {
+    int first;            // rows until the first change of group
+    __device__ __forceinline__ void issue(uint32_t stage, uint8_t* generic, const Columns& C, int lane) {
         constexpr int WORDS = Cfg<1, ST>::WORDS;
+        const bool fresh = left == 0;  // this warp's first block of its group: its scales too
         if constexpr (VEC) {
-            const uint32_t base = op::smem_u32(stage);
-            if ((lane & 3) * 32 < limit) {
-                const uint32_t dst = base + (lane >> 2) * 128 + (lane & 3) * 16;
-                const uint8_t* p = q;
-                const bool whole = row + kBlock <= K;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {  // t = i: line half i & 1, lines from (i / 2) 8, chunks swapped by i & 2
-                    if (whole || row + i * 8 + (lane >> 2) < K)
-                        op::cp_async<16>((dst + (i >> 1) * 1024 + (i & 1) * 64) ^ ((i & 2) * 16), p);
-                    p += 8 * row_bytes;
+            const uint32_t dst = stage + chunk_at(lane >> 2, lane & 3);
+            const long long step = 8 * row_bytes;
+            const uint8_t *p1 = q + step, *p2 = p1 + step, *p3 = p2 + step;
+            if (in) {
+                if (rows >= kBlock) {
+                    op::cp_async<16>(dst, q);
+                    op::cp_async<16>(dst + 512, p1);
+                    op::cp_async<16>(dst + 1024, p2);
+                    op::cp_async<16>(dst + 1536, p3);
+                } else {
+                    const int n = rows - (lane >> 2);
+                    if (n > 0) op::cp_async<16>(dst, q);
+                    if (n > 8) op::cp_async<16>(dst + 512, p1);
+                    if (n > 16) op::cp_async<16>(dst + 1024, p2);
+                    if (n > 24) op::cp_async<16>(dst + 1536, p3);
                 }
             }
-            if (fresh && lane * 4 < limit)
-                op::cp_async<4 * (int)sizeof(ST)>(base + WORDS + lane * 4 * (int)sizeof(ST), s);
-            q += kBlock * row_bytes;
+            q = p3 + step;
+            if (fresh && in_s) op::cp_async<4 * (int)sizeof(ST)>(stage + WORDS + lane * 4 * (int)sizeof(ST), s);
         } else {
-            const int t = lane & 3, g = lane >> 2;
-            const int nb = min(8, (limit - col + 1) >> 1);  // limit and col are even: whole bytes
+            if (lane < rows) {  // the 64 bytes of the lane's row; col and limit are even: whole bytes
+                for (int c = 0; c < 4; ++c) {
+                    const int col = C.first(c & 2) + (c & 1) * 32;
+                    const int nb = min(16, (C.end(c & 2) - col) >> 1);
+                    const uint8_t* p = q + (col >> 1);
+                    uint32_t v[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                uint32_t lo = 0u, hi = 0u;
-                if (row + 8 * t + i < K) {
-                    const uint8_t* p = q + (row + 8 * t + i) * row_bytes + (col >> 1);
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        if (b < nb) lo |= (uint32_t)__ldg(p + b) << (8 * b);
-                        if (4 + b < nb) hi |= (uint32_t)__ldg(p + 4 + b) << (8 * b);
-                    }
+                    for (int b = 0; b < 16; ++b)
+                        if (b < nb) v[b >> 2] |= (uint32_t)__ldg(p + b) << (8 * (b & 3));
+                    *reinterpret_cast<uint4*>(generic + chunk_at(lane, c)) = make_uint4(v[0], v[1], v[2], v[3]);
                 }
-                *reinterpret_cast<uint2*>(stage + word_at(i, g, t)) = make_uint2(lo, hi);
             }
-            ST* d = reinterpret_cast<ST*>(stage + WORDS) + g * 16 + t * 4;
+            q += kBlock * row_bytes;
+            ST* d = reinterpret_cast<ST*>(generic + WORDS) + lane * 4;
+            const int cs = C.first(lane & 16) + (lane & 15) * 4;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (fresh && col + 4 * t + j < limit) d[j] = s[col + 4 * t + j];
+                if (fresh && cs + j < C.end(lane & 16)) d[j] = s[cs + j];
         }
-        row += kBlock;
+        rows -= kBlock;
+        if (fresh) left = first, first = group;
         left -= kBlock;
-        fresh = left == 0;
-        if (fresh) {
-            left = group;
-            s += N;
-        }
+        if (left == 0) s += N;
     }
 };
 
-// Column (of a thread's 16) that accumulator tile i holds in its first row
-// (c0, c1); its second row (c2, c3) is two columns on.  Odd tiles hold 16
-// times their sum.
-__device__ __forceinline__ constexpr int tile_col(int i) { return (i >> 1) * 4 + (i & 1); }
+// Column (of the warp's 128) that accumulator tile i of lane group g holds in
+// its first row (c0, c1); its second row (c2, c3) is two columns on.  Odd
+// tiles hold 16 times their sum.
+__device__ __forceinline__ constexpr int tile_col(int i, int g) { return (i >> 1) * 32 + 4 * g + (i & 1); }
 
-// acc += one block: 32 rows of x (f16, xs + 8 t of this thread's token g) and
-// this thread's words; bias: the block's -8 2^-24 sum(x) per token.
+// acc += one block: 32 rows of x (xa: shared address of this lane's values of
+// its token, in the order of x_place) and the warp's stage; sc: the scales of
+// the lane's columns.
 template <int NT8>
-__device__ __forceinline__ void block_fma(float (&acc)[NT8][8][4], const uint2 (&w)[8], const float (&sc)[16],
-                                          const __half* xs, const float* bias, int g, int t) {
+__device__ __forceinline__ void block_fma(float (&acc)[NT8][8][4], uint32_t stage, const float (&sc)[16],
+                                          const uint32_t (&xa)[NT8], uint32_t x_off) {
     uint32_t b[NT8][4];
-    float2 c0[NT8];
 #pragma unroll
-    for (int n = 0; n < NT8; ++n) {
-        const uint4 v = *reinterpret_cast<const uint4*>(xs + (n * 8 + g) * kXStride + 8 * t);
-        b[n][0] = v.x, b[n][1] = v.y, b[n][2] = v.z, b[n][3] = v.w;
-        c0[n] = *reinterpret_cast<const float2*>(bias + n * 8 + 2 * t);
-    }
+    for (int n = 0; n < NT8; ++n) op::lds128(b[n], xa[n] + x_off);
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {  // columns 4 h .. 4 h + 3: half (h & 1) of word h / 2
-        uint32_t u[4];             // rows (0,1), (2,3), (4,5), (6,7) interleaved
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const uint32_t r0 = h < 2 ? w[2 * p].x : w[2 * p].y, r1 = h < 2 ? w[2 * p + 1].x : w[2 * p + 1].y;
-            u[p] = __byte_perm(r0, r1, (h & 1) ? 0x7632 : 0x5410);
-        }
+    for (int h = 0; h < 4; ++h) {  // columns 32 h .. 32 h + 31, four of them this lane's
+        uint32_t u[4];             // rows 2 t + (0, 1), then 8, 16 and 24 on
+        op::ldmatrix_trans(u, stage ^ (h * 16));
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const uint32_t mask = s ? 0x00f000f0u : 0x000f000fu, flip = s ? 0x00800080u : 0x00080008u;
@@ -240,8 +244,7 @@ __device__ __forceinline__ void block_fma(float (&acc)[NT8][8][4], const uint2 (
 #pragma unroll
             for (int n = 0; n < NT8; ++n) {
                 float d[4];
-                const float k = s ? 16.f : 1.f;
-                mma_f16(d, a[0], a[1], a[2], a[3], b[n][0], b[n][1], k * c0[n].x, k * c0[n].y);
+                mma_f16(d, a[0], a[1], a[2], a[3], b[n][0], b[n][1]);
                 mma_f16_add(d, a[4], a[5], a[6], a[7], b[n][2], b[n][3]);
                 float(&o)[4] = acc[n][2 * h + s];
                 o[0] = fmaf(sa, d[0], o[0]);
@@ -253,6 +256,28 @@ __device__ __forceinline__ void block_fma(float (&acc)[NT8][8][4], const uint2 (
     }
 }
 
+// The bias of some blocks of one group: acc -= scale * (8 2^-24 sum x), bias
+// holding the factors of this lane's two tokens (16 times that on odd tiles).
+template <int NT8>
+__device__ __forceinline__ void bias_fma(float (&acc)[NT8][8][4], const float (&sc)[16], const float2 (&bias)[NT8]) {
+#pragma unroll
+    for (int n = 0; n < NT8; ++n)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float k = (i & 1) ? 16.f : 1.f, bx = k * bias[n].x, by = k * bias[n].y;
+            const float sa = sc[4 * (i >> 1) + (i & 1)], sb = sc[4 * (i >> 1) + (i & 1) + 2];
+            float(&o)[4] = acc[n][i];
+            o[0] = fmaf(sa, bx, o[0]);
+            o[1] = fmaf(sa, by, o[1]);
+            o[2] = fmaf(sb, bx, o[2]);
+            o[3] = fmaf(sb, by, o[3]);
+        }
+}
+
+// Where row r of a 32-row block of x is staged: lane t's eight values of the
+// block's two products (rows 2 t + (0, 1), and 8, 16, 24 on) side by side.
+__device__ __forceinline__ constexpr int x_place(int r) { return ((r >> 1) & 3) * 8 + (r >> 3) * 2 + (r & 1); }
+
 // The f16 a value is staged as, and the power of two a bf16 row is
 // multiplied with (f16 rows: 1).
 __device__ __forceinline__ float row_factor(float amax) {
@@ -262,163 +287,175 @@ __device__ __forceinline__ float row_factor(float amax) {
     return __uint_as_float((uint32_t)(p + 127) << 23);
 }
 
-// Stage rows [row0, row0 + rows) of nt tokens (rows of x, ldx apart) as f16,
-// zeros up to a whole number of blocks, and each block's bias.  bf16 rows are
-// multiplied by factor[token]; where the piece is all of the quarter (own),
-// the factor is found here.  The quarter's two warps (half = 0, 1) take the
-// tokens in turn, 8 neighbouring values per lane.  Tokens past nt are left as
-// they are: a token is a column of the products, and what such a column holds
-// reaches no other.
-template <int NT8, typename XT>
-__device__ __forceinline__ void stage_x(__half* xs, float* bias, const XT* x, long long ldx, int nt, int row0, int rows,
-                                        float* factor, bool own, int half, int lane) {
-    const int span = (rows + kBlock - 1) / kBlock * kBlock;
+// Stage rows [row0, row0 + rows) of nt tokens (rows of x, ldx apart; stride:
+// the staged rows') as f16, zeros up to a whole number of blocks, and each
+// block's bias.  bf16 rows are multiplied by their factor (lane tok's).  One
+// warp, 8 neighbouring values per lane.  Tokens past nt are not staged: a
+// token is a column of the products, and what such a column holds reaches no
+// other.
+template <typename XT>
+__device__ __forceinline__ void stage_x(__half* xs, int stride, float* bias, int pair, const XT* x, long long ldx, int nt,
+                                        int row0, int rows, float factors, int lane) {
     const bool vec = (ldx & 7) == 0;  // rows (and so 8 values) start on 16 bytes
-    constexpr int PASSES = kPiece / 256;
-#pragma unroll 2
-    for (int tok = half; tok < nt; tok += 2) {
-        const XT* xr = x + tok * ldx + row0;
-        float v[PASSES][8];
+    const int span = (rows + kBlock - 1) & ~(kBlock - 1);
+    const int per = (span + 255) >> 8;  // passes of 256 rows
+#pragma unroll 4
+    for (int i = 0; i < nt * per; ++i) {
+        const int tok = per == 1 ? i : i / per, r = (i - tok * per) * 256 + lane * 8;
+        const XT* xr = x + tok * ldx + row0 + r;
+        float v[8];
+        if (vec && r + 8 <= rows) {
+            XT tmp[8];
+            *reinterpret_cast<uint4*>(tmp) = *reinterpret_cast<const uint4*>(xr);
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int r = p * 256 + lane * 8;
-            if (vec && r + 8 <= rows) {
+            for (int j = 0; j < 8; ++j) v[j] = to_f32(tmp[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = r + j < rows ? to_f32(xr[j]) : 0.f;
+        }
+        float f = 1.f;
+        if constexpr (!std::is_same<XT, __half>::value) f = __shfl_sync(0xffffffffu, factors, tok);
+        __half2 h[4];
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            h[j] = __floats2half2_rn(v[2 * j] * f, v[2 * j + 1] * f);
+            const float2 b = __half22float2(h[j]);
+            s += b.x + b.y;
+        }
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        if (r < span) {
+            __half* o = xs + tok * stride + (r & ~31);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<__half2*>(o + x_place((r & 31) + 2 * j)) = h[j];
+            if ((lane & 3) == 0) bias[(r / kBlock) * pair + tok] = s * -0x1p-21f;  // -8 2^-24
+        }
+    }
+}
+
+// Lane tok: the factor of token tok over rows [r0, r1).  One warp.
+template <typename XT>
+__device__ __forceinline__ float find_factors(const XT* x, long long ldx, int nt, int r0, int r1, int lane) {
+    const bool vec = (ldx & 7) == 0;  // r0 is a multiple of 8
+    float mine = 1.f;
+    for (int tok = 0; tok < nt; ++tok) {
+        const XT* xr = x + tok * ldx;
+        float m = 0.f;
+        int r = r0 + lane * 8;
+        if (vec) {
+#pragma unroll 4
+            for (; r + 8 <= r1; r += 256) {
                 XT tmp[8];
                 *reinterpret_cast<uint4*>(tmp) = *reinterpret_cast<const uint4*>(xr + r);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[p][j] = to_f32(tmp[j]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[p][j] = r + j < rows ? to_f32(xr[r + j]) : 0.f;
+                for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(to_f32(tmp[j])));
             }
         }
-        float f = 1.f;
-        if constexpr (!std::is_same<XT, __half>::value) {
-            if (own) {
-                float m = 0.f;
+        for (; r < r1; r += 256)  // without vectors, or the end of the rows
 #pragma unroll
-                for (int p = 0; p < PASSES; ++p)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[p][j]));
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                f = row_factor(m);
-                if (lane == 0) factor[tok] = f;
-            } else {
-                f = factor[tok];
-            }
-        }
-#pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int r = p * 256 + lane * 8;
-            __half2 h[4];
-            float s = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                h[j] = __floats2half2_rn(v[p][2 * j] * f, v[p][2 * j + 1] * f);
-                const float2 b = __half22float2(h[j]);
-                s += b.x + b.y;
-            }
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            s += __shfl_xor_sync(0xffffffffu, s, 2);
-            if (r < span) {
-                *reinterpret_cast<uint4*>(xs + tok * kXStride + r) = *reinterpret_cast<const uint4*>(h);
-                if ((lane & 3) == 0) bias[(r / kBlock) * NT8 * 8 + tok] = s * -0x1p-21f;  // -8 2^-24
-            }
-        }
-    }
-}
-
-// Each token's factor over rows [r0, r1) (bf16 tokens, more than one piece).
-template <typename XT>
-__device__ __forceinline__ void find_factors(float* factor, const XT* x, long long ldx, int nt, int r0, int r1, int half,
-                                             int lane) {
-    for (int tok = half; tok < nt; tok += 2) {
-        float m = 0.f;
-#pragma unroll 8
-        for (int k = r0 + lane; k < r1; k += 32) m = fmaxf(m, fabsf(to_f32(x[tok * ldx + k])));
+            for (int j = 0; j < 8; ++j) m = fmaxf(m, r + j < r1 ? fabsf(to_f32(xr[r + j])) : 0.f);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) factor[tok] = row_factor(m);
+        if (lane == tok) mine = row_factor(m);
     }
+    return mine;
 }
 
-// The sums of this CTA's slice [k0, k1) of K, left in smem as [token][256
-// columns] fp32 (column c of half c / 128 is col0 + c or col1 + c - 128) for
-// the nt tokens.  limit0 / limit1: the first column of each half that does
-// not exist.  before_x: called once the first weight loads are on their way,
-// before x is read.
+// The sums of this CTA's slice [k0, k1) of K, left in smem as [token][128
+// columns] fp32 for the nt tokens.  before_x: called once the first weight
+// loads are on their way, before x is read.
 template <int NT8, typename XT, typename ST, bool VEC, typename F>
-__device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, int col0, int limit0, int col1, int limit1,
-                                           const XT* x, long long ldx, int nt, int k0, int k1, F&& before_x) {
-    using C = Cfg<NT8, ST>;
+__device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, const Columns& C, const XT* x, long long ldx,
+                                           int nt, int k0, int k1, F&& before_x) {
+    using Cf = Cfg<NT8, ST>;
     constexpr bool BF = !std::is_same<XT, __half>::value;
-    __shared__ float s_factor[kQuarters][NT8 * 8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const int half = warp & 1, quarter = warp >> 1;
-    __half* xs = reinterpret_cast<__half*>(smem + quarter * (C::X + C::BIAS));
-    float* bias = reinterpret_cast<float*>(smem + quarter * (C::X + C::BIAS) + C::X);
-    uint8_t* ring = smem + kQuarters * (C::X + C::BIAS) + warp * (C::STAGES * C::STAGE);
+    uint8_t* ring = smem + warp * Cf::RING;
     const int nblk = (k1 - k0 + kBlock - 1) / kBlock;
-    const int r0 = k0 + nblk * quarter / kQuarters * kBlock;
-    const int r1 = min(k1, k0 + nblk * (quarter + 1) / kQuarters * kBlock);
+    const int r0 = k0 + nblk * warp / kWarps * kBlock;
+    const int r1 = min(k1, k0 + nblk * (warp + 1) / kWarps * kBlock);
     Loader<ST, VEC> ld;
-    ld.start(W, half ? col1 : col0, half ? limit1 : limit0, r0, r1, lane);
-    int put = 0, get = 0;
-    auto issue = [&] {
-        if (ld.row < r1) ld.issue(ring + put * C::STAGE, lane);
+    ld.start(W, C, r0, lane);
+    int todo = nblk * (warp + 1) / kWarps - nblk * warp / kWarps;  // blocks to load
+    const uint32_t ring0 = op::smem_u32(ring);
+    auto issue = [&](uint32_t at) {  // at: the stage's place in the ring
+        if (--todo >= 0) ld.issue(ring0 + at, ring + at, C, lane);
         op::cp_commit();  // (an empty group where nothing is left keeps the count)
-        put = put + 1 == C::STAGES ? 0 : put + 1;
     };
 #pragma unroll
-    for (int i = 0; i < C::STAGES - 1; ++i) issue();
+    for (int i = 0; i < Cf::STAGES - 1; ++i) issue(i * Cf::STAGE);
     before_x();
+    // this warp's part of x: nt rows, 64 bytes apart in the banks, and block sums
+    const int piece = piece_rows(nt, Cf::X), stride = piece + 32, pair = (nt + 1) & ~1;
+    __half* xs = reinterpret_cast<__half*>(smem + kWarps * Cf::RING + warp * Cf::X);
+    float* bias = reinterpret_cast<float*>(xs + nt * stride);
     float acc[NT8][8][4];
+    int xo[NT8], bo[NT8];  // columns past nt repeat the last token
 #pragma unroll
-    for (int n = 0; n < NT8; ++n)
+    for (int n = 0; n < NT8; ++n) {
+        xo[n] = min(n * 8 + g, nt - 1) * stride + 8 * t;
+        bo[n] = min(n * 8 + 2 * t, pair - 2);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[n][i][c] = 0.f;
-    const bool own = r1 - r0 <= kPiece;
-    if (BF && !own) find_factors(s_factor[quarter], x, ldx, nt, r0, r1, half, lane);  // (a token's warp reads it back)
-    const int words = word_at(0, g, t);
+    }
+    float factors = 1.f;
+    if (BF && r0 < r1) factors = find_factors(x, ldx, nt, r0, r1, lane);
+    const uint32_t rows0 = ring0 + chunk_at(lane, 0);  // a matrix load's address: row l % 8 of row group l / 8
+    const uint32_t sc0 = ring0 + Cf::WORDS + 4 * g * (int)sizeof(ST);
     float sc[16];
-    int left = 0;  // rows that the scales at hand still cover
-    for (int row0 = r0; row0 < r1; row0 += kPiece) {
-        const int rows = min(kPiece, r1 - row0);
-        if (row0 > r0) op::pair_sync(1 + quarter);  // the last piece of x has been read
-        else __syncwarp();
-        stage_x<NT8>(xs, bias, x, ldx, nt, row0, rows, s_factor[quarter], own, half, lane);
-        op::pair_sync(1 + quarter);
-        for (int b = 0; b * kBlock < rows; ++b) {
-            op::cp_wait<C::STAGES - 2>();
-            __syncwarp();  // the copies are other lanes'
-            const uint8_t* stage = ring + get * C::STAGE;
-            get = get + 1 == C::STAGES ? 0 : get + 1;
-            uint2 w[8];
+    float2 b8[NT8];  // the bias not yet taken off, of the scales at hand
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint2*>(stage + words + i * 128);
-            if (left == 0) {  // a group's first block brings its scales
-                const ST* sp = reinterpret_cast<const ST*>(stage + C::WORDS) + g * 16;
-                constexpr int V = 16 / (int)sizeof(ST);
+    for (int n = 0; n < NT8; ++n) b8[n] = make_float2(0.f, 0.f);
+    int left = 0, next = W.group - r0 % W.group;  // rows that the scales at hand still cover; of the next ones
+    for (int row0 = r0; row0 < r1; row0 += piece) {
+        const int rows = min(piece, r1 - row0);
+        __syncwarp();  // the last piece of x has been read
+        stage_x(xs, stride, bias, pair, x, ldx, nt, row0, rows, factors, lane);
+        uint32_t xa[NT8], ba[NT8];
 #pragma unroll
-                for (int i = 0; i < 16 / V; ++i) {
-                    ST tmp[V];
-                    *reinterpret_cast<uint4*>(tmp) = reinterpret_cast<const uint4*>(sp)[i];
+        for (int n = 0; n < NT8; ++n) xa[n] = op::smem_u32(xs + xo[n]), ba[n] = op::smem_u32(bias + bo[n]);
+        // turns of the ring: the piece is a multiple of it, so a turn starts at its first stage
+        for (int r = 0; r < rows; r += Cf::STAGES * kBlock) {
 #pragma unroll
-                    for (int j = 0; j < V; ++j) sc[i * V + j] = to_f32(tmp[j]);
+            for (int j = 0; j < Cf::STAGES; ++j) {
+                if (r + j * kBlock >= rows) break;
+                op::cp_wait<Cf::STAGES - 2>();
+                __syncwarp();  // the copies (and the staged x) are other lanes'
+                if (left == 0) {  // a group's first block brings its scales
+                    if (row0 + r + j * kBlock > r0) bias_fma<NT8>(acc, sc, b8);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        ST v[4];
+                        op::lds<4 * (int)sizeof(ST)>(v, sc0 + j * Cf::STAGE + 32 * h * (int)sizeof(ST));
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) sc[4 * h + c] = to_f32(v[c]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT8; ++n) b8[n] = make_float2(0.f, 0.f);
+                    left = next;
+                    next = W.group;
                 }
-                left = W.group - (row0 + b * kBlock) % W.group;
+                left -= kBlock;
+                // (the copies issued here go to the stage read one turn ago: every
+                // lane has passed this turn's __syncwarp since)
+                issue((j + Cf::STAGES - 1) % Cf::STAGES * Cf::STAGE);
+                block_fma<NT8>(acc, rows0 + j * Cf::STAGE, sc, xa, j * kBlock * 2);
+#pragma unroll
+                for (int n = 0; n < NT8; ++n) {
+                    float2 v;
+                    op::lds<8>(&v, ba[n] + j * pair * 4);
+                    b8[n].x += v.x, b8[n].y += v.y;
+                }
             }
-            left -= kBlock;
-            // (the copies issued here go to the stage read one turn ago: every
-            // lane has passed this turn's __syncwarp since)
-            issue();
-            block_fma<NT8>(acc, w, sc, xs + b * kBlock, bias + b * NT8 * 8, g, t);
+#pragma unroll
+            for (int n = 0; n < NT8; ++n) xa[n] += Cf::STAGES * kBlock * 2, ba[n] += Cf::STAGES * pair * 4;
         }
     }
+    if (r0 < r1) bias_fma<NT8>(acc, sc, b8);
     op::cp_wait<0>();
     __syncthreads();
     // the quarters' sums, in their order
@@ -428,18 +465,19 @@ __device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, i
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int tok = n * 8 + 2 * t + (c & 1);
+            float f = 1.f;
+            if constexpr (BF) f = 1.0f / __shfl_sync(0xffffffffu, factors, tok);
             if (tok < nt) {
-                const float f = BF && r0 < r1 ? 1.0f / s_factor[quarter][tok] : 1.0f;
-                float* o = red + (quarter * NT8 * 8 + tok) * kCols + half * 128 + 16 * g + (c & 2);
+                float* o = red + (warp * NT8 * 8 + tok) * kCols + (c & 2);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[tile_col(i)] = acc[n][i][c] * ((i & 1) ? 0x1p20f : 0x1p24f) * f;
+                for (int i = 0; i < 8; ++i) o[tile_col(i, g)] = acc[n][i][c] * ((i & 1) ? 0x1p20f : 0x1p24f) * f;
             }
         }
     __syncthreads();
     for (int i = threadIdx.x; i < nt * kCols; i += kThreads) {
         float v = red[i];
 #pragma unroll
-        for (int q = 1; q < kQuarters; ++q) v += red[q * NT8 * 8 * kCols + i];
+        for (int q = 1; q < kWarps; ++q) v += red[q * NT8 * 8 * kCols + i];
         red[i] = v;  // read and written by this thread alone
     }
 }
@@ -460,12 +498,13 @@ __host__ __device__ __forceinline__ int slice_row(int K, int r, int lg) {
     return k < K ? k : K;
 }
 
-// Slices of K (a power of two) for a launch of `tiles` tiles: a CTA for every
-// SM, a block at least for each quarter, at most a portable cluster.
-__host__ __forceinline__ int slices(long long tiles, int K, int sms) {
+// Slices of K (a power of two) for a launch of `tiles` tiles: as many CTAs as
+// the SMs hold at once (per_sm each), a block at least for each warp, at most
+// a portable cluster.
+__host__ __forceinline__ int slices(long long tiles, int K, int sms, int per_sm) {
     const int blocks = (K + kBlock - 1) / kBlock;
     int S = 1;
-    while (S < 8 && tiles * S < sms && blocks >= 2 * S * kQuarters) S *= 2;
+    while (S < 8 && 2 * tiles * S <= (long long)per_sm * sms && blocks >= 2 * S * kWarps) S *= 2;
     return S;
 }
 
@@ -482,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT8, ST>::PER_SM) int4_matvec_ke
     const int t0 = blockIdx.y * NT8 * 8, nt = min(NT8 * 8, T - t0);
     const int k0 = slice_row(W.K, slice, lg), k1 = slice_row(W.K, slice + 1, lg);
     const XT* xt = x + (long long)t0 * W.K;
-    slice_sums<NT8, XT, ST, VEC>(mv_smem, W, col0, W.N, col0 + 128, W.N, xt, W.K, nt, k0, k1, [] {});
+    const Columns C{col0, col0 + kHalf, W.N, W.N};
+    slice_sums<NT8, XT, ST, VEC>(mv_smem, W, C, xt, W.K, nt, k0, k1, [] {});
     float* red = reinterpret_cast<float*>(mv_smem);
     if (S > 1) op::cluster_sync();
     else __syncthreads();
@@ -555,10 +595,10 @@ __device__ __forceinline__ bool find_unit(const GroupTable* tab, int u, int& gro
 
 // Gate/up: h = silu(c a_gate) (c a_up), c the row's scale (its sigmoid gate).
 // Down: the fp32 sums, un-permuted.  Grid: (column tiles, units, slices); a
-// gate/up tile is 128 hidden columns (gate in the first half, up in the
-// second), a down tile 256 columns.
+// gate/up tile is 64 hidden columns (gate in the first half, up in the
+// second), a down tile 128 columns.
 template <typename ST, bool GATE_UP>
-__global__ void __launch_bounds__(kThreads, 2) experts_kernel(const GroupTable* tab, int num_experts, int group_rows,
+__global__ void __launch_bounds__(kThreads, Cfg<1, ST>::PER_SM) experts_kernel(const GroupTable* tab, int num_experts, int group_rows,
                                                            const __grid_constant__ Experts E, const Rows R) {
     op::pdl_enter();
     extern __shared__ __align__(128) uint8_t mv_smem[];
@@ -568,24 +608,24 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(const GroupTable* 
     const int nt = min(8, tab->rows[grp] - row), row0 = tab->row0[grp] + row;
     const int K = R.K[sh], N = R.N[sh];
     const int F = N / 2;
-    const int col0 = blockIdx.x * (GATE_UP ? 128 : kCols);
+    const int col0 = blockIdx.x * (GATE_UP ? kHalf : kCols);
     if (col0 >= (GATE_UP ? F : N)) return;
     const int S = gridDim.z, slice = blockIdx.z, lg = __ffs(S) - 1;
     const int k0 = slice_row(K, slice, lg), k1 = slice_row(K, slice + 1, lg);
     const Weight<ST> W{E.q[expert], static_cast<const ST*>(E.s[expert]), N / 2, N, K, group_rows};
-    slice_sums<1, __half, ST, true>(mv_smem, W, col0, GATE_UP ? F : N, GATE_UP ? F + col0 : col0 + 128, N,
-                                    R.x[sh] + (long long)row0 * K, K, nt, k0, k1, [] {});
+    const Columns C{col0, GATE_UP ? F + col0 : col0 + kHalf, GATE_UP ? F : N, N};
+    slice_sums<1, __half, ST, true>(mv_smem, W, C, R.x[sh] + (long long)row0 * K, K, nt, k0, k1, [] {});
     const float* red = reinterpret_cast<const float*>(mv_smem);
     if (S > 1) op::cluster_sync();
     else __syncthreads();
-    const int width = GATE_UP ? 128 : kCols, items = nt * width;
+    const int width = GATE_UP ? kHalf : kCols, items = nt * width;
     const int i0 = (items >> lg) * slice, i1 = i0 + (items >> lg);  // items is a multiple of 8
     for (int i = i0 + threadIdx.x; i < i1; i += kThreads) {
         const int tok = i / width, c = i % width;
         if (GATE_UP) {
             if (col0 + c >= F) continue;
             const float g = R.scale[sh] ? R.scale[sh][row0 + tok] : 1.0f;
-            const float a = g * cluster_total(red, tok * kCols + c, S), b = g * cluster_total(red, tok * kCols + 128 + c, S);
+            const float a = g * cluster_total(red, tok * kCols + c, S), b = g * cluster_total(red, tok * kCols + kHalf + c, S);
             const float hv = __fdividef(a, 1.0f + __expf(-a)) * b;
             if (!(fabsf(hv) < 65520.0f)) atomicOr(R.err, kErrF16Range);  // rounds to infinity in f16
             R.h[sh][(long long)(row0 + tok) * F + col0 + c] = __float2half_rn(hv);

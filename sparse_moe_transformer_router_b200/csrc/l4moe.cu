@@ -734,9 +734,9 @@ l4moe_status run_layer(l4moe_handle* h, int T, const void* x, const void* Wr, co
             // tiles of 8 rows: every routed one holds an entry
             const int units = (has ? std::min(Tv, std::min(E, Tv) + Tv / 8) : 0) + (T + 7) / 8;
             if (units > 65535) return fail(h, L4MOE_ERR_ARG, "batch too long for experts with group scales");
-            const int gt = (std::max(has ? F : 0, Fs) + 127) / 128, dt = (d + mv::kCols - 1) / mv::kCols;
-            const int sg = mv::slices((long long)gt * units, d, h->sms);
-            const int sd = mv::slices((long long)dt * units, has ? std::min(F, Fs) : Fs, h->sms);
+            const int gt = (std::max(has ? F : 0, Fs) + mv::kHalf - 1) / mv::kHalf, dt = (d + mv::kCols - 1) / mv::kCols;
+            const int sg = mv::slices((long long)gt * units, d, h->sms, 4);
+            const int sd = mv::slices((long long)dt * units, has ? std::min(F, Fs) : Fs, h->sms, 4);
             fill(grouped->gate_up, grouped->shared_gate_up, 0);
             {
                 LaunchTimer t_gu(h, 3, st);

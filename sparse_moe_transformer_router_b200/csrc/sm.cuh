@@ -43,6 +43,27 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
+// BYTES (8 or 16) from a shared address to a local value.
+template <int BYTES>
+__device__ __forceinline__ void lds(void* v, uint32_t addr) {
+    uint32_t* r = static_cast<uint32_t*>(v);
+    if constexpr (BYTES == 16)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+    else asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void lds128(uint32_t (&r)[4], uint32_t addr) { lds<16>(r, addr); }
+
+// Four 8 x 8 matrices of 16-bit units, transposed: lane l gives the address of
+// row l % 8 of matrix l / 8 (16 bytes); r[m] gets units (2 (l % 4), l / 4) and
+// (2 (l % 4) + 1, l / 4) of matrix m.
+__device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
 // The two warps that share named barrier `id` (1 to 15).
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 
