@@ -24,12 +24,13 @@
 //   [0, 15] left where it lies in the f16's low bits is the subnormal u 2^-24
 //   (or 16 u 2^-24 one nibble up), exact in the tensor core.  No conversion
 //   instruction, 0.625 per weight in all.
-// - The bias 8 leaves as -8 sum(x) (2^-24) times the group's scale, from the
-//   tokens' block sums kept beside them, once for each run of a group's blocks.
+// - The bias 8 leaves as -8 sum(x) (2^-24) times the group's scale, once for
+//   each run of a group's blocks; the sums are two products with a constant.
 // - The block's fp32 sum is multiplied by the group's scale and added to the
 //   column's total in fp32: the weights are never rounded to a product.
-// - Tokens are f16 in shared memory: f16 rows as they are, bf16 rows divided
-//   by a power of two that brings the largest of a quarter slice to [2^14, 2^15)
+// - Tokens come along in the ring, f16 rows as they are, bf16 rows divided (on
+//   their way to the product) by a power of two that brings the largest of a
+//   warp's rows to [2^14, 2^15)
 //   (exact for values down to 2^-31 of it, others round at 2^-39 of it).
 //   A row with an infinity or a NaN gives NaN (inf times the bias).
 //
@@ -57,30 +58,21 @@ constexpr int kCols = 128;       // columns of a CTA: two halves of 64
 constexpr int kHalf = kCols / 2;
 constexpr int kBlock = 32;       // rows of a block (scale groups are multiples of it)
 
-// A warp's shared memory: its part of x (f16) with the block sums, and a ring
-// of weight blocks (32 rows of 64 bytes, then the scales of the columns).
+// A warp's ring of blocks: 32 rows of 64 bytes of the weight, the scales of
+// the columns, 64 bytes (32 rows) of each token.
 template <int NT8, typename ST>
 struct Cfg {
     static constexpr int WORDS = kBlock * 64;
-    static constexpr int STAGE = WORDS + kCols * (int)sizeof(ST);
+    static constexpr int XOFF = WORDS + kCols * (int)sizeof(ST);
+    static constexpr int STAGE = XOFF + NT8 * 8 * 64;
     static constexpr int STAGES = 4;
     static constexpr int RING = STAGES * STAGE;
-    static constexpr int X = NT8 * 4864;  // 256 rows of NT8 * 8 tokens, more of fewer (piece_rows)
     // CTAs that share an SM: the registers' limit (up to 8 tokens 128 a
     // thread, 16 tokens 168)
     static constexpr int PER_SM = NT8 == 1 ? 4 : 3;
     static constexpr int RED = (int)sizeof(float) * kWarps * NT8 * 8 * kCols;  // over all of it
-    static constexpr int USED = kWarps * (X + RING);
-    static constexpr int SMEM = USED > RED ? USED : RED;
+    static constexpr int SMEM = kWarps * RING > RED ? kWarps * RING : RED;
 };
-
-// Rows of x that a warp stages at a time: as many (a multiple of 128) as
-// nt token rows, 64 bytes apart in the banks, and their block sums (of whole
-// pairs of tokens) leave room for.
-__host__ __device__ __forceinline__ int piece_rows(int nt, int bytes) {
-    const int pair = (nt + 1) & ~1;
-    return (bytes - 64 * nt) / (256 * nt + 16 * pair) * 128;
-}
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -116,8 +108,9 @@ struct Weight {
     int K, group;
 };
 
-// Where a stage holds the 16 bytes of columns 32 c .. 32 c + 31 of row r: the
-// eight rows of a matrix load lie in different banks.
+// Where a stage holds the 16 bytes of columns 32 c .. 32 c + 31 of row r (or of
+// rows 8 c .. 8 c + 7 of token r): the eight rows of a matrix load lie in
+// different banks.
 __device__ __forceinline__ constexpr int chunk_at(int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); }
 
 // The 128 columns of a CTA: two runs of 64, each with the first column that
@@ -213,24 +206,76 @@ struct Loader {
     }
 };
 
+// The tokens' rows as one lane loads them: 8 values (16 bytes) of tokens
+// l / 4, l / 4 + 8.  Rows past the slice's end are zeros; tokens past nt are
+// not loaded (a token is a column of the products, and what such a column
+// holds reaches no other).
+template <int NT8, typename XT>
+struct XLoader {
+    const XT* x;      // this lane's 8 values of token l / 4 in the next block
+    long long ldx;
+    int rows;         // rows left from this lane's on
+    bool vec;         // rows (and so 8 values) start on 16 bytes
+
+    __device__ __forceinline__ void start(const XT* x0, long long ld, int row, int end, int lane) {
+        ldx = ld;
+        vec = (ld & 7) == 0;
+        x = x0 + (lane >> 2) * ld + row + (lane & 3) * 8;
+        rows = end - row - (lane & 3) * 8;
+    }
+    __device__ __forceinline__ void issue(uint32_t at, uint8_t* generic, int nt, int lane) {
+#pragma unroll
+        for (int n = 0; n < NT8; ++n) {
+            const int off = n * 8 * 64 + chunk_at(lane >> 2, lane & 3);
+            if ((lane >> 2) + 8 * n < nt) {
+                const XT* p = x + n * 8 * ldx;
+                if (vec) {
+                    op::cp_async16_zero(at + off, p, rows > 0);  // 8 values or none: rows of a multiple of 8
+                } else {
+                    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < rows) w[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[j] << (16 * (j & 1));
+                    *reinterpret_cast<uint4*>(generic + off) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+        x += kBlock;
+        rows -= kBlock;
+    }
+};
+
 // Column (of the warp's 128) that accumulator tile i of lane group g holds in
 // its first row (c0, c1); its second row (c2, c3) is two columns on.  Odd
 // tiles hold 16 times their sum.
 __device__ __forceinline__ constexpr int tile_col(int i, int g) { return (i >> 1) * 32 + 4 * g + (i & 1); }
 
-// acc += one block: 32 rows of x (xa: shared address of this lane's values of
-// its token, in the order of x_place) and the warp's stage; sc: the scales of
-// the lane's columns.
-template <int NT8>
-__device__ __forceinline__ void block_fma(float (&acc)[NT8][8][4], uint32_t stage, const float (&sc)[16],
-                                          const uint32_t (&xa)[NT8], uint32_t x_off) {
+// acc += one block: the warp's stage (rows_at: this lane's address of a matrix
+// load of the weight, x_at: of the tokens); sc: the scales of the lane's
+// columns; f: what the lane's tokens (column l / 4 of each 8) are multiplied
+// with as they become f16.  b8 += -8 2^-24 sum(x) of the lane's two tokens: a
+// product with rows of that constant (an f16 subnormal).
+template <int NT8, bool BF>
+__device__ __forceinline__ void block_fma(float (&acc)[NT8][8][4], float (&b8)[NT8][4], uint32_t rows_at, uint32_t x_at,
+                                          const float (&sc)[16], const float (&f)[NT8]) {
+    constexpr uint32_t kMinus8 = 0x80088008u;
     uint32_t b[NT8][4];
 #pragma unroll
-    for (int n = 0; n < NT8; ++n) op::lds128(b[n], xa[n] + x_off);
+    for (int n = 0; n < NT8; ++n) {
+        op::ldmatrix(b[n], x_at + n * 8 * 64);
+        if constexpr (BF) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __half2 h = __floats2half2_rn(__uint_as_float(b[n][j] << 16) * f[n],
+                                                    __uint_as_float(b[n][j] & 0xffff0000u) * f[n]);
+                b[n][j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+    }
 #pragma unroll
     for (int h = 0; h < 4; ++h) {  // columns 32 h .. 32 h + 31, four of them this lane's
         uint32_t u[4];             // rows 2 t + (0, 1), then 8, 16 and 24 on
-        op::ldmatrix_trans(u, stage ^ (h * 16));
+        op::ldmatrix_trans(u, rows_at ^ (h * 16));
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const uint32_t mask = s ? 0x00f000f0u : 0x000f000fu, flip = s ? 0x00800080u : 0x00080008u;
@@ -254,17 +299,22 @@ __device__ __forceinline__ void block_fma(float (&acc)[NT8][8][4], uint32_t stag
             }
         }
     }
+#pragma unroll
+    for (int n = 0; n < NT8; ++n) {
+        mma_f16_add(b8[n], kMinus8, kMinus8, kMinus8, kMinus8, b[n][0], b[n][1]);
+        mma_f16_add(b8[n], kMinus8, kMinus8, kMinus8, kMinus8, b[n][2], b[n][3]);
+    }
 }
 
-// The bias of some blocks of one group: acc -= scale * (8 2^-24 sum x), bias
-// holding the factors of this lane's two tokens (16 times that on odd tiles).
+// The bias of some blocks of one group: acc += scale * b8 (16 times that on
+// odd tiles).
 template <int NT8>
-__device__ __forceinline__ void bias_fma(float (&acc)[NT8][8][4], const float (&sc)[16], const float2 (&bias)[NT8]) {
+__device__ __forceinline__ void bias_fma(float (&acc)[NT8][8][4], const float (&sc)[16], const float (&b8)[NT8][4]) {
 #pragma unroll
     for (int n = 0; n < NT8; ++n)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float k = (i & 1) ? 16.f : 1.f, bx = k * bias[n].x, by = k * bias[n].y;
+            const float k = (i & 1) ? 16.f : 1.f, bx = k * b8[n][0], by = k * b8[n][1];
             const float sa = sc[4 * (i >> 1) + (i & 1)], sb = sc[4 * (i >> 1) + (i & 1) + 2];
             float(&o)[4] = acc[n][i];
             o[0] = fmaf(sa, bx, o[0]);
@@ -273,10 +323,6 @@ __device__ __forceinline__ void bias_fma(float (&acc)[NT8][8][4], const float (&
             o[3] = fmaf(sb, by, o[3]);
         }
 }
-
-// Where row r of a 32-row block of x is staged: lane t's eight values of the
-// block's two products (rows 2 t + (0, 1), and 8, 16, 24 on) side by side.
-__device__ __forceinline__ constexpr int x_place(int r) { return ((r >> 1) & 3) * 8 + (r >> 3) * 2 + (r & 1); }
 
 // The f16 a value is staged as, and the power of two a bf16 row is
 // multiplied with (f16 rows: 1).
@@ -287,76 +333,73 @@ __device__ __forceinline__ float row_factor(float amax) {
     return __uint_as_float((uint32_t)(p + 127) << 23);
 }
 
-// Stage rows [row0, row0 + rows) of nt tokens (rows of x, ldx apart; stride:
-// the staged rows') as f16, zeros up to a whole number of blocks, and each
-// block's bias.  bf16 rows are multiplied by their factor (lane tok's).  One
-// warp, 8 neighbouring values per lane.  Tokens past nt are not staged: a
-// token is a column of the products, and what such a column holds reaches no
-// other.
+// 8 values of a row of x from row r on (rows from `rows` on are zeros), as
+// 16 bytes of its type.
 template <typename XT>
-__device__ __forceinline__ void stage_x(__half* xs, int stride, float* bias, int pair, const XT* x, long long ldx, int nt,
-                                        int row0, int rows, float factors, int lane) {
-    const bool vec = (ldx & 7) == 0;  // rows (and so 8 values) start on 16 bytes
-    const int span = (rows + kBlock - 1) & ~(kBlock - 1);
-    const int per = (span + 255) >> 8;  // passes of 256 rows
-#pragma unroll 4
-    for (int i = 0; i < nt * per; ++i) {
-        const int tok = per == 1 ? i : i / per, r = (i - tok * per) * 256 + lane * 8;
-        const XT* xr = x + tok * ldx + row0 + r;
-        float v[8];
-        if (vec && r + 8 <= rows) {
-            XT tmp[8];
-            *reinterpret_cast<uint4*>(tmp) = *reinterpret_cast<const uint4*>(xr);
+__device__ __forceinline__ uint4 load_x8(const XT* xr, int r, int rows, bool vec) {
+    if (vec && r + 8 <= rows) return *reinterpret_cast<const uint4*>(xr + r);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(xr + r);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = to_f32(tmp[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = r + j < rows ? to_f32(xr[j]) : 0.f;
-        }
-        float f = 1.f;
-        if constexpr (!std::is_same<XT, __half>::value) f = __shfl_sync(0xffffffffu, factors, tok);
-        __half2 h[4];
-        float s = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            h[j] = __floats2half2_rn(v[2 * j] * f, v[2 * j + 1] * f);
-            const float2 b = __half22float2(h[j]);
-            s += b.x + b.y;
-        }
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        if (r < span) {
-            __half* o = xs + tok * stride + (r & ~31);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) *reinterpret_cast<__half2*>(o + x_place((r & 31) + 2 * j)) = h[j];
-            if ((lane & 3) == 0) bias[(r / kBlock) * pair + tok] = s * -0x1p-21f;  // -8 2^-24
-        }
-    }
+    for (int j = 0; j < 8; ++j)
+        if (r + j < rows) w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Lane tok: the factor of token tok over rows [r0, r1).  One warp.
-template <typename XT>
-__device__ __forceinline__ float find_factors(const XT* x, long long ldx, int nt, int r0, int r1, int lane) {
-    const bool vec = (ldx & 7) == 0;  // r0 is a multiple of 8
-    float mine = 1.f;
-    for (int tok = 0; tok < nt; ++tok) {
-        const XT* xr = x + tok * ldx;
-        float m = 0.f;
-        int r = r0 + lane * 8;
-        if (vec) {
-#pragma unroll 4
-            for (; r + 8 <= r1; r += 256) {
-                XT tmp[8];
-                *reinterpret_cast<uint4*>(tmp) = *reinterpret_cast<const uint4*>(xr + r);
+// The largest magnitude among 8 bf16 values and m.
+__device__ __forceinline__ float absmax8(uint4 v, float m) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(to_f32(tmp[j])));
+    for (int j = 0; j < 4; ++j) {
+        m = fmaxf(m, fabsf(__uint_as_float(w[j] << 16)));
+        m = fmaxf(m, fabsf(__uint_as_float(w[j] & 0xffff0000u)));
+    }
+    return m;
+}
+__device__ __forceinline__ float warp_max(float m) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+
+// Lane tok: the factor of bf16 token tok over rows [r0, r1).  One warp, with
+// eight 16-byte loads of a lane on their way at once: of 512 rows of four
+// tokens, or of one token's next 2048 rows.
+__device__ __forceinline__ float find_factors(const __nv_bfloat16* x, long long ldx, int nt, int r0, int r1, int lane) {
+    const bool vec = (ldx & 7) == 0;
+    const int rows = r1 - r0;
+    float mine = 1.f;
+    if (rows <= 512) {
+        for (int tok0 = 0; tok0 < nt; tok0 += 4) {
+            uint4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int tok = tok0 + (j >> 1), r = (j & 1) * 256 + lane * 8;
+                v[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (tok < nt && r < rows) v[j] = load_x8(x + tok * ldx + r0, r, rows, vec);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float m = warp_max(absmax8(v[2 * j + 1], absmax8(v[2 * j], 0.f)));
+                if (lane == tok0 + j) mine = row_factor(m);
             }
         }
-        for (; r < r1; r += 256)  // without vectors, or the end of the rows
+        return mine;
+    }
+    for (int tok = 0; tok < nt; ++tok) {
+        float m = 0.f;
+        for (int p = 0; p < rows; p += 2048) {
+            uint4 v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = fmaxf(m, r + j < r1 ? fabsf(to_f32(xr[r + j])) : 0.f);
+            for (int j = 0; j < 8; ++j) {
+                const int r = p + j * 256 + lane * 8;
+                v[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < rows) v[j] = load_x8(x + tok * ldx + r0, r, rows, vec);
+            }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            for (int j = 0; j < 8; ++j) m = absmax8(v[j], m);
+        }
+        m = warp_max(m);
         if (lane == tok) mine = row_factor(m);
     }
     return mine;
@@ -378,84 +421,73 @@ __device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, c
     const int r1 = min(k1, k0 + nblk * (warp + 1) / kWarps * kBlock);
     Loader<ST, VEC> ld;
     ld.start(W, C, r0, lane);
-    int todo = nblk * (warp + 1) / kWarps - nblk * warp / kWarps;  // blocks to load
+    const int blocks = nblk * (warp + 1) / kWarps - nblk * warp / kWarps;
     const uint32_t ring0 = op::smem_u32(ring);
-    auto issue = [&](uint32_t at) {  // at: the stage's place in the ring
-        if (--todo >= 0) ld.issue(ring0 + at, ring + at, C, lane);
-        op::cp_commit();  // (an empty group where nothing is left keeps the count)
-    };
 #pragma unroll
-    for (int i = 0; i < Cf::STAGES - 1; ++i) issue(i * Cf::STAGE);
+    for (int i = 0; i < Cf::STAGES - 1; ++i)
+        if (i < blocks) ld.issue(ring0 + i * Cf::STAGE, ring + i * Cf::STAGE, C, lane);
     before_x();
-    // this warp's part of x: nt rows, 64 bytes apart in the banks, and block sums
-    const int piece = piece_rows(nt, Cf::X), stride = piece + 32, pair = (nt + 1) & ~1;
-    __half* xs = reinterpret_cast<__half*>(smem + kWarps * Cf::RING + warp * Cf::X);
-    float* bias = reinterpret_cast<float*>(xs + nt * stride);
-    float acc[NT8][8][4];
-    int xo[NT8], bo[NT8];  // columns past nt repeat the last token
+    XLoader<NT8, XT> xl;
+    xl.start(x, ldx, r0, r1, lane);
+#pragma unroll
+    for (int i = 0; i < Cf::STAGES - 1; ++i)
+        if (i < blocks) xl.issue(ring0 + i * Cf::STAGE + Cf::XOFF, ring + i * Cf::STAGE + Cf::XOFF, nt, lane);
+    // the first stages are one group; empty groups keep the count of the later ones
+#pragma unroll
+    for (int i = 0; i < Cf::STAGES - 1; ++i) op::cp_commit();
+    float factors = 1.f, f[NT8];
+    if constexpr (BF) {
+        if (blocks > 0) factors = find_factors(x, ldx, nt, r0, r1, lane);
+    }
+    float acc[NT8][8][4], b8[NT8][4];  // b8: the bias not yet added, of the scales at hand
 #pragma unroll
     for (int n = 0; n < NT8; ++n) {
-        xo[n] = min(n * 8 + g, nt - 1) * stride + 8 * t;
-        bo[n] = min(n * 8 + 2 * t, pair - 2);
+        f[n] = __shfl_sync(0xffffffffu, factors, n * 8 + g);
+        b8[n][0] = b8[n][1] = b8[n][2] = b8[n][3] = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[n][i][c] = 0.f;
     }
-    float factors = 1.f;
-    if (BF && r0 < r1) factors = find_factors(x, ldx, nt, r0, r1, lane);
-    const uint32_t rows0 = ring0 + chunk_at(lane, 0);  // a matrix load's address: row l % 8 of row group l / 8
+    // a matrix load's addresses: row l % 8 of row group l / 8 of the weight; token l % 8, rows 8 (l / 8) on
+    const uint32_t rows0 = ring0 + chunk_at(lane, 0), x0 = ring0 + Cf::XOFF + chunk_at(lane & 7, lane >> 3);
     const uint32_t sc0 = ring0 + Cf::WORDS + 4 * g * (int)sizeof(ST);
     float sc[16];
-    float2 b8[NT8];  // the bias not yet taken off, of the scales at hand
-#pragma unroll
-    for (int n = 0; n < NT8; ++n) b8[n] = make_float2(0.f, 0.f);
     int left = 0, next = W.group - r0 % W.group;  // rows that the scales at hand still cover; of the next ones
-    for (int row0 = r0; row0 < r1; row0 += piece) {
-        const int rows = min(piece, r1 - row0);
-        __syncwarp();  // the last piece of x has been read
-        stage_x(xs, stride, bias, pair, x, ldx, nt, row0, rows, factors, lane);
-        uint32_t xa[NT8], ba[NT8];
+    for (int i0 = 0; i0 < blocks; i0 += Cf::STAGES) {
 #pragma unroll
-        for (int n = 0; n < NT8; ++n) xa[n] = op::smem_u32(xs + xo[n]), ba[n] = op::smem_u32(bias + bo[n]);
-        // turns of the ring: the piece is a multiple of it, so a turn starts at its first stage
-        for (int r = 0; r < rows; r += Cf::STAGES * kBlock) {
+        for (int j = 0; j < Cf::STAGES; ++j) {
+            if (i0 + j >= blocks) break;
+            op::cp_wait<Cf::STAGES - 2>();
+            __syncwarp();  // the copies are other lanes'
+            if (left == 0) {  // a group's first block brings its scales
+                if (i0 + j > 0) bias_fma<NT8>(acc, sc, b8);
 #pragma unroll
-            for (int j = 0; j < Cf::STAGES; ++j) {
-                if (r + j * kBlock >= rows) break;
-                op::cp_wait<Cf::STAGES - 2>();
-                __syncwarp();  // the copies (and the staged x) are other lanes'
-                if (left == 0) {  // a group's first block brings its scales
-                    if (row0 + r + j * kBlock > r0) bias_fma<NT8>(acc, sc, b8);
+                for (int h = 0; h < 4; ++h) {
+                    ST v[4];
+                    op::lds<4 * (int)sizeof(ST)>(v, sc0 + j * Cf::STAGE + 32 * h * (int)sizeof(ST));
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        ST v[4];
-                        op::lds<4 * (int)sizeof(ST)>(v, sc0 + j * Cf::STAGE + 32 * h * (int)sizeof(ST));
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) sc[4 * h + c] = to_f32(v[c]);
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT8; ++n) b8[n] = make_float2(0.f, 0.f);
-                    left = next;
-                    next = W.group;
+                    for (int c = 0; c < 4; ++c) sc[4 * h + c] = to_f32(v[c]);
                 }
-                left -= kBlock;
-                // (the copies issued here go to the stage read one turn ago: every
-                // lane has passed this turn's __syncwarp since)
-                issue((j + Cf::STAGES - 1) % Cf::STAGES * Cf::STAGE);
-                block_fma<NT8>(acc, rows0 + j * Cf::STAGE, sc, xa, j * kBlock * 2);
 #pragma unroll
-                for (int n = 0; n < NT8; ++n) {
-                    float2 v;
-                    op::lds<8>(&v, ba[n] + j * pair * 4);
-                    b8[n].x += v.x, b8[n].y += v.y;
-                }
+                for (int n = 0; n < NT8; ++n) b8[n][0] = b8[n][1] = b8[n][2] = b8[n][3] = 0.f;
+                left = next;
+                next = W.group;
             }
-#pragma unroll
-            for (int n = 0; n < NT8; ++n) xa[n] += Cf::STAGES * kBlock * 2, ba[n] += Cf::STAGES * pair * 4;
+            left -= kBlock;
+            // (these copies go to the stage read one turn ago: every lane has
+            // passed this turn's __syncwarp since)
+            constexpr int LAST = Cf::STAGES - 1;
+            const int to = (j + LAST) % Cf::STAGES * Cf::STAGE;
+            if (i0 + j + LAST < blocks) {
+                ld.issue(ring0 + to, ring + to, C, lane);
+                xl.issue(ring0 + to + Cf::XOFF, ring + to + Cf::XOFF, nt, lane);
+            }
+            op::cp_commit();
+            block_fma<NT8, BF>(acc, b8, rows0 + j * Cf::STAGE, x0 + j * Cf::STAGE, sc, f);
         }
     }
-    if (r0 < r1) bias_fma<NT8>(acc, sc, b8);
+    if (blocks > 0) bias_fma<NT8>(acc, sc, b8);
     op::cp_wait<0>();
     __syncthreads();
     // the quarters' sums, in their order
@@ -465,12 +497,12 @@ __device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, c
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int tok = n * 8 + 2 * t + (c & 1);
-            float f = 1.f;
-            if constexpr (BF) f = 1.0f / __shfl_sync(0xffffffffu, factors, tok);
+            float inv = 1.f;
+            if constexpr (BF) inv = 1.0f / __shfl_sync(0xffffffffu, factors, tok);
             if (tok < nt) {
                 float* o = red + (warp * NT8 * 8 + tok) * kCols + (c & 2);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[tile_col(i, g)] = acc[n][i][c] * ((i & 1) ? 0x1p20f : 0x1p24f) * f;
+                for (int i = 0; i < 8; ++i) o[tile_col(i, g)] = acc[n][i][c] * ((i & 1) ? 0x1p20f : 0x1p24f) * inv;
             }
         }
     __syncthreads();

@@ -735,8 +735,8 @@ l4moe_status run_layer(l4moe_handle* h, int T, const void* x, const void* Wr, co
             const int units = (has ? std::min(Tv, std::min(E, Tv) + Tv / 8) : 0) + (T + 7) / 8;
             if (units > 65535) return fail(h, L4MOE_ERR_ARG, "batch too long for experts with group scales");
             const int gt = (std::max(has ? F : 0, Fs) + mv::kHalf - 1) / mv::kHalf, dt = (d + mv::kCols - 1) / mv::kCols;
-            const int sg = mv::slices((long long)gt * units, d, h->sms, 4);
-            const int sd = mv::slices((long long)dt * units, has ? std::min(F, Fs) : Fs, h->sms, 4);
+            const int sg = mv::slices((long long)gt * units, d, h->sms, mv::Cfg<1, float>::PER_SM);
+            const int sd = mv::slices((long long)dt * units, has ? std::min(F, Fs) : Fs, h->sms, mv::Cfg<1, float>::PER_SM);
             fill(grouped->gate_up, grouped->shared_gate_up, 0);
             {
                 LaunchTimer t_gu(h, 3, st);

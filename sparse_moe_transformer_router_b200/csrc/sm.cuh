@@ -37,6 +37,10 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
     if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
     else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
+// 16 bytes, or zeros (and no read) where ok is false.
+__device__ __forceinline__ void cp_async16_zero(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT>
 __device__ __forceinline__ void cp_wait() {
@@ -52,7 +56,16 @@ __device__ __forceinline__ void lds(void* v, uint32_t addr) {
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
     else asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void lds128(uint32_t (&r)[4], uint32_t addr) { lds<16>(r, addr); }
+
+// Four 8 x 8 matrices of 16-bit units: lane l gives the address of row l % 8
+// of matrix l / 8 (16 bytes); r[m] gets units 2 (l % 4), 2 (l % 4) + 1 of row
+// l / 4 of matrix m.
+__device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
 
 // Four 8 x 8 matrices of 16-bit units, transposed: lane l gives the address of
 // row l % 8 of matrix l / 8 (16 bytes); r[m] gets units (2 (l % 4), l / 4) and
