@@ -21,10 +21,10 @@ l4moe_status op_fail(l4moe_status s, const char* msg) noexcept;
 // it (pdl_enter) before touching memory, which hides the launch gaps of the
 // short kernels of a small batch.  Launch errors are left for
 // cudaGetLastError, like a <<<>>> launch.
-// cluster_z > 0 also launches the grid as clusters of (1, 1, cluster_z).
+// cluster.x > 0 also launches the grid as clusters of that shape.
 template <typename... KArgs, typename... Args>
-void launch_kc(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-               unsigned cluster_z, Args&&... args) {
+void launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                    const unsigned (&cluster)[3], Args&&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -34,15 +34,29 @@ void launch_kc(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cud
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = 1;
-    if (cluster_z > 0) {
+    if (cluster[0] > 0) {
         attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = 1;
-        attr[1].val.clusterDim.y = 1;
-        attr[1].val.clusterDim.z = cluster_z;
+        attr[1].val.clusterDim.x = cluster[0];
+        attr[1].val.clusterDim.y = cluster[1];
+        attr[1].val.clusterDim.z = cluster[2];
         cfg.numAttrs = 2;
     }
     cfg.attrs = attr;
     cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Clusters of (1, 1, cluster_z), or of (cluster_x, 1, 1); 0: none.
+template <typename... KArgs, typename... Args>
+void launch_kc(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+               unsigned cluster_z, Args&&... args) {
+    const unsigned c[3] = {cluster_z > 0 ? 1u : 0u, 1u, cluster_z};
+    launch_cluster(kernel, grid, block, smem, st, c, std::forward<Args>(args)...);
+}
+template <typename... KArgs, typename... Args>
+void launch_cluster_x(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                      unsigned cluster_x, Args&&... args) {
+    const unsigned c[3] = {cluster_x, 1u, 1u};
+    launch_cluster(kernel, grid, block, smem, st, c, std::forward<Args>(args)...);
 }
 
 template <typename... KArgs, typename... Args>

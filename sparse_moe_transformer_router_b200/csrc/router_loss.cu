@@ -26,11 +26,15 @@ int device_sms() {
     return sms;
 }
 
-// Blocks of the sums: every warp has a row group to take, at most 2 blocks
-// per SM (a partial of each is added by the finishing block).
+// Blocks of the sums: every warp has a row group to take; up to two passes of
+// a cluster's blocks stay one cluster (one launch: a second costs about as
+// much as a pass), more are spread over the SMs, whose partials the finishing
+// block adds.
 int loss_blocks(int T, int E, int sms) {
     const long long rows = (long long)kLossWarps * (32 / lanes_of(E));  // per block and pass
-    return (int)std::max(1LL, std::min<long long>((T + rows - 1) / rows, 2LL * sms));
+    const long long need = std::max(1LL, (T + rows - 1) / rows);
+    if (need <= 2 * kLossCluster) return (int)std::min<long long>(need, kLossCluster);
+    return (int)std::min<long long>(need, 2LL * sms);
 }
 
 l4moe_status cuda_error(cudaError_t e, const char* what) {
@@ -79,11 +83,12 @@ struct LossArgs {
 
 template <typename IT, int L, bool SIG>
 void launch_loss(const LossArgs& a, cudaStream_t st) {
-    launch_k(router_loss_kernel<IT, L, SIG>, dim3(a.blocks), dim3(kLossThreads), 0, st,
-             static_cast<const IT*>(a.logits), a.ld, a.T, a.E, a.k, a.vec ? 1 : 0, a.mask, a.idx, a.wb, a.wz, a.part,
-             a.result);
-    if (a.blocks > 1)
-        launch_k(router_loss_finish_kernel, dim3(1), dim3(256), 0, st, (const float*)a.part, a.blocks, a.E, a.k, a.wb,
+    const bool alone = a.blocks <= kLossCluster;
+    launch_cluster_x(router_loss_kernel<IT, L, SIG>, dim3(a.blocks), dim3(kLossThreads), 0, st,
+                     alone && a.blocks > 1 ? (unsigned)a.blocks : 0u, static_cast<const IT*>(a.logits), a.ld, a.T, a.E,
+                     a.k, a.vec ? 1 : 0, a.mask, a.idx, a.wb, a.wz, a.part, a.result);
+    if (!alone)
+        launch_k(router_loss_finish_kernel, dim3(1), dim3(1024), 0, st, (const float*)a.part, a.blocks, a.E, a.k, a.wb,
                  a.wz, a.result);
 }
 
@@ -101,7 +106,7 @@ struct GradArgs {
 
 template <typename IT, int L, bool SIG>
 void launch_grad(const GradArgs& a, cudaStream_t st) {
-    launch_k(router_loss_grad_kernel<IT, L, SIG>, dim3(a.blocks), dim3(kLossThreads), 0, st,
+    launch_k(router_loss_grad_kernel<IT, L, SIG>, dim3(a.blocks), dim3(kGradThreads), 0, st,
              static_cast<const IT*>(a.logits), a.ld, a.T, a.E, a.vec ? 1 : 0, a.mask, a.result, a.upstream,
              static_cast<IT*>(a.dl), a.ldd);
 }
@@ -186,7 +191,7 @@ l4moe_status l4moe_router_loss_grad(int T, int E, const void* logits, l4moe_elem
     if (T == 0) return L4MOE_OK;
     const int sms = device_sms();
     if (sms < 1) return op_fail(L4MOE_ERR_CUDA, "l4moe_router_loss_grad: no CUDA device");
-    const long long rows = (long long)kLossWarps * (32 / lanes_of(E));
+    const long long rows = (long long)(kGradThreads / 32) * (32 / lanes_of(E));
     const int blocks = (int)std::min<long long>((T + rows - 1) / rows, 8LL * sms);
     GradArgs a{logits, ld, T, E, mask, result, upstream, dlogits, ldd, blocks,
                vectors(E, logits, ld, type) && vectors(E, dlogits, ldd, type)};
