@@ -206,21 +206,38 @@ struct Loader {
     }
 };
 
+// The token rows of a CTA: rows of x, ld apart, from row0 on, or those that
+// slot row0 + token of perm names (entry / k).
+template <typename XT>
+struct Tokens {
+    const XT* x;
+    long long ld;
+    int row0;
+    const int32_t* perm;
+    int k;
+    __device__ __forceinline__ const XT* row(int token) const {
+        const int r = perm ? perm[row0 + token] / k : row0 + token;
+        return x + r * ld;
+    }
+};
+
 // The tokens' rows as one lane loads them: 8 values (16 bytes) of tokens
 // l / 4, l / 4 + 8.  Rows past the slice's end are zeros; tokens past nt are
 // not loaded (a token is a column of the products, and what such a column
 // holds reaches no other).
 template <int NT8, typename XT>
 struct XLoader {
-    const XT* x;      // this lane's 8 values of token l / 4 in the next block
-    long long ldx;
-    int rows;         // rows left from this lane's on
-    bool vec;         // rows (and so 8 values) start on 16 bytes
+    const XT* x[NT8];  // this lane's 8 values of tokens l / 4, l / 4 + 8 in the next block
+    int rows;          // rows left from this lane's on
+    bool vec;          // rows (and so 8 values) start on 16 bytes
 
-    __device__ __forceinline__ void start(const XT* x0, long long ld, int row, int end, int lane) {
-        ldx = ld;
-        vec = (ld & 7) == 0;
-        x = x0 + (lane >> 2) * ld + row + (lane & 3) * 8;
+    __device__ __forceinline__ void start(const Tokens<XT>& X, int nt, int row, int end, int lane) {
+        vec = (X.ld & 7) == 0;
+#pragma unroll
+        for (int n = 0; n < NT8; ++n) {
+            const int tok = n * 8 + (lane >> 2);
+            x[n] = X.row(tok < nt ? tok : 0) + row + (lane & 3) * 8;
+        }
         rows = end - row - (lane & 3) * 8;
     }
     __device__ __forceinline__ void issue(uint32_t at, uint8_t* generic, int nt, int lane) {
@@ -228,7 +245,7 @@ struct XLoader {
         for (int n = 0; n < NT8; ++n) {
             const int off = n * 8 * 64 + chunk_at(lane >> 2, lane & 3);
             if ((lane >> 2) + 8 * n < nt) {
-                const XT* p = x + n * 8 * ldx;
+                const XT* p = x[n];
                 if (vec) {
                     op::cp_async16_zero(at + off, p, rows > 0);  // 8 values or none: rows of a multiple of 8
                 } else {
@@ -239,8 +256,8 @@ struct XLoader {
                     *reinterpret_cast<uint4*>(generic + off) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
+            x[n] += kBlock;
         }
-        x += kBlock;
         rows -= kBlock;
     }
 };
@@ -363,54 +380,41 @@ __device__ __forceinline__ float warp_max(float m) {
 }
 
 // Lane tok: the factor of bf16 token tok over rows [r0, r1).  One warp, with
-// eight 16-byte loads of a lane on their way at once: of 512 rows of four
-// tokens, or of one token's next 2048 rows.
-__device__ __forceinline__ float find_factors(const __nv_bfloat16* x, long long ldx, int nt, int r0, int r1, int lane) {
-    const bool vec = (ldx & 7) == 0;
-    const int rows = r1 - r0;
-    float mine = 1.f;
-    if (rows <= 512) {
-        for (int tok0 = 0; tok0 < nt; tok0 += 4) {
-            uint4 v[8];
+// eight 16-byte loads of a lane on their way at once.
+__device__ __forceinline__ float find_factors(const Tokens<__nv_bfloat16>& X, int nt, int r0, int r1, int lane) {
+    const bool vec = (X.ld & 7) == 0;
+    const int rows = r1 - r0, per = (rows + 255) >> 8;  // loads of 256 rows per token
+    float mine = 1.f, m = 0.f;
+    int tok = 0, p = 0, tok_j = 0, p_j = 0;  // the next load's token and pass; the next one's to use
+    for (int i0 = 0; i0 < nt * per; i0 += 8) {
+        uint4 v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int tok = tok0 + (j >> 1), r = (j & 1) * 256 + lane * 8;
-                v[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (tok < nt && r < rows) v[j] = load_x8(x + tok * ldx + r0, r, rows, vec);
-            }
+        for (int j = 0; j < 8; ++j) {
+            v[j] = make_uint4(0u, 0u, 0u, 0u);
+            const int r = p * 256 + lane * 8;
+            if (tok < nt && r < rows) v[j] = load_x8(X.row(tok) + r0, r, rows, vec);
+            if (++p == per) p = 0, ++tok;
+        }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float m = warp_max(absmax8(v[2 * j + 1], absmax8(v[2 * j], 0.f)));
-                if (lane == tok0 + j) mine = row_factor(m);
+        for (int j = 0; j < 8; ++j) {
+            m = absmax8(v[j], m);
+            if (++p_j == per) {
+                m = warp_max(m);
+                if (lane == tok_j) mine = row_factor(m);
+                m = 0.f;
+                p_j = 0, ++tok_j;
             }
         }
-        return mine;
-    }
-    for (int tok = 0; tok < nt; ++tok) {
-        float m = 0.f;
-        for (int p = 0; p < rows; p += 2048) {
-            uint4 v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int r = p + j * 256 + lane * 8;
-                v[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < rows) v[j] = load_x8(x + tok * ldx + r0, r, rows, vec);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m = absmax8(v[j], m);
-        }
-        m = warp_max(m);
-        if (lane == tok) mine = row_factor(m);
     }
     return mine;
 }
 
 // The sums of this CTA's slice [k0, k1) of K, left in smem as [token][128
-// columns] fp32 for the nt tokens.  before_x: called once the first weight
-// loads are on their way, before x is read.
+// columns] fp32 for the nt tokens.  tokens(): the token rows, asked for once
+// the first weight loads are on their way.
 template <int NT8, typename XT, typename ST, bool VEC, typename F>
-__device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, const Columns& C, const XT* x, long long ldx,
-                                           int nt, int k0, int k1, F&& before_x) {
+__device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, const Columns& C, int nt, int k0, int k1,
+                                           F&& tokens) {
     using Cf = Cfg<NT8, ST>;
     constexpr bool BF = !std::is_same<XT, __half>::value;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -426,9 +430,9 @@ __device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, c
 #pragma unroll
     for (int i = 0; i < Cf::STAGES - 1; ++i)
         if (i < blocks) ld.issue(ring0 + i * Cf::STAGE, ring + i * Cf::STAGE, C, lane);
-    before_x();
+    const Tokens<XT> X = tokens();
     XLoader<NT8, XT> xl;
-    xl.start(x, ldx, r0, r1, lane);
+    xl.start(X, nt, r0, r1, lane);
 #pragma unroll
     for (int i = 0; i < Cf::STAGES - 1; ++i)
         if (i < blocks) xl.issue(ring0 + i * Cf::STAGE + Cf::XOFF, ring + i * Cf::STAGE + Cf::XOFF, nt, lane);
@@ -437,7 +441,7 @@ __device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, c
     for (int i = 0; i < Cf::STAGES - 1; ++i) op::cp_commit();
     float factors = 1.f, f[NT8];
     if constexpr (BF) {
-        if (blocks > 0) factors = find_factors(x, ldx, nt, r0, r1, lane);
+        if (blocks > 0) factors = find_factors(X, nt, r0, r1, lane);
     }
     float acc[NT8][8][4], b8[NT8][4];  // b8: the bias not yet added, of the scales at hand
 #pragma unroll
@@ -552,9 +556,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT8, ST>::PER_SM) int4_matvec_ke
     const int col0 = blockIdx.x * kCols;
     const int t0 = blockIdx.y * NT8 * 8, nt = min(NT8 * 8, T - t0);
     const int k0 = slice_row(W.K, slice, lg), k1 = slice_row(W.K, slice + 1, lg);
-    const XT* xt = x + (long long)t0 * W.K;
     const Columns C{col0, col0 + kHalf, W.N, W.N};
-    slice_sums<NT8, XT, ST, VEC>(mv_smem, W, C, xt, W.K, nt, k0, k1, [] {});
+    slice_sums<NT8, XT, ST, VEC>(mv_smem, W, C, nt, k0, k1, [&] { return Tokens<XT>{x, W.K, t0, nullptr, 1}; });
     float* red = reinterpret_cast<float*>(mv_smem);
     if (S > 1) op::cluster_sync();
     else __syncthreads();
@@ -581,12 +584,15 @@ struct Experts {
 
 // A launch's rows and outputs for its routed experts and the shared one.
 struct Rows {
-    const __half* x[2];      // operand rows: routed (slot order), shared (token order)
+    const void* x[2];        // operand rows: routed (slot order, or x itself: gather), shared (token order)
     int K[2], N[2];          // the weights' rows and columns
     const float* scale[2];   // gate/up: what multiplies a row's sums (null: 1)
     __half* h[2];            // gate/up: hidden rows [., N / 2]
     float* part[2];          // down: fp32 rows [., N], routed at the row's entry (perm)
     const int32_t* perm;
+    int k;
+    bool gather;             // routed operand row = x[perm[slot] / k]
+    int shared_rows;         // > 0: the shared expert's rows, its units the first ones (it is not in the list)
     unsigned* err;
 };
 
@@ -629,15 +635,29 @@ __device__ __forceinline__ bool find_unit(const GroupTable* tab, int u, int& gro
 // Down: the fp32 sums, un-permuted.  Grid: (column tiles, units, slices); a
 // gate/up tile is 64 hidden columns (gate in the first half, up in the
 // second), a down tile 128 columns.
-template <typename ST, bool GATE_UP>
-__global__ void __launch_bounds__(kThreads, Cfg<1, ST>::PER_SM) experts_kernel(const GroupTable* tab, int num_experts, int group_rows,
-                                                           const __grid_constant__ Experts E, const Rows R) {
-    op::pdl_enter();
+template <typename XT, typename ST, bool GATE_UP>
+__global__ void __launch_bounds__(kThreads, Cfg<1, ST>::PER_SM) experts_kernel(const GroupTable* tab, int num_experts,
+                                                                              int group_rows,
+                                                                              const __grid_constant__ Experts E,
+                                                                              const Rows R) {
     extern __shared__ __align__(128) uint8_t mv_smem[];
-    int grp, row;
-    if (!find_unit(tab, blockIdx.y, grp, row)) return;
-    const int expert = tab->expert[grp], sh = expert == num_experts ? 1 : 0;
-    const int nt = min(8, tab->rows[grp] - row), row0 = tab->row0[grp] + row;
+    // the shared expert's units come first and read nothing that the routing
+    // before this launch writes: they need not wait for it
+    const int shared_units = (R.shared_rows + 7) >> 3;
+    const bool early = GATE_UP && (int)blockIdx.y < shared_units;
+    if (!early) op::pdl_wait();
+    op::pdl_launch();
+    int expert, sh, nt, row0;
+    if ((int)blockIdx.y < shared_units) {
+        expert = num_experts, sh = 1;
+        row0 = blockIdx.y * 8;
+        nt = min(8, R.shared_rows - row0);
+    } else {
+        int grp, row;
+        if (!find_unit(tab, blockIdx.y - shared_units, grp, row)) return;
+        expert = tab->expert[grp], sh = expert == num_experts ? 1 : 0;
+        nt = min(8, tab->rows[grp] - row), row0 = tab->row0[grp] + row;
+    }
     const int K = R.K[sh], N = R.N[sh];
     const int F = N / 2;
     const int col0 = blockIdx.x * (GATE_UP ? kHalf : kCols);
@@ -646,7 +666,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<1, ST>::PER_SM) experts_kernel(c
     const int k0 = slice_row(K, slice, lg), k1 = slice_row(K, slice + 1, lg);
     const Weight<ST> W{E.q[expert], static_cast<const ST*>(E.s[expert]), N / 2, N, K, group_rows};
     const Columns C{col0, GATE_UP ? F + col0 : col0 + kHalf, GATE_UP ? F : N, N};
-    slice_sums<1, __half, ST, true>(mv_smem, W, C, R.x[sh] + (long long)row0 * K, K, nt, k0, k1, [] {});
+    slice_sums<1, XT, ST, true>(mv_smem, W, C, nt, k0, k1, [&] {
+        return Tokens<XT>{static_cast<const XT*>(R.x[sh]), K, row0, GATE_UP && R.gather && !sh ? R.perm : nullptr, R.k};
+    });
     const float* red = reinterpret_cast<const float*>(mv_smem);
     if (S > 1) op::cluster_sync();
     else __syncthreads();

@@ -28,6 +28,7 @@
 #include "moe_gemm.cuh"
 #include "permute.cuh"
 #include "quant.cuh"
+#include "route_group.cuh"
 #include "route_small.cuh"
 #include "router.cuh"
 
@@ -467,22 +468,23 @@ struct ExpertWeights {
     const void *shared_gate_up, *shared_down;
 };
 
-template <typename ST, bool GATE_UP>
+template <typename XT, typename ST, bool GATE_UP>
 void launch_experts_t(dim3 grid, cudaStream_t st, const GroupTable* tab, int E, int group, const mv::Experts& ptrs,
                       const mv::Rows& rows) {
     constexpr size_t smem = mv::Cfg<1, ST>::SMEM;
     static std::atomic<uint64_t> attr_done{0};
-    ensure_smem_attr(attr_done, mv::experts_kernel<ST, GATE_UP>, smem);
-    launch_kc(mv::experts_kernel<ST, GATE_UP>, grid, dim3(mv::kThreads), smem, st, grid.z > 1 ? grid.z : 0u, tab, E,
-              group, ptrs, rows);
+    ensure_smem_attr(attr_done, mv::experts_kernel<XT, ST, GATE_UP>, smem);
+    launch_kc(mv::experts_kernel<XT, ST, GATE_UP>, grid, dim3(mv::kThreads), smem, st, grid.z > 1 ? grid.z : 0u, tab,
+              E, group, ptrs, rows);
 }
 
-template <bool GATE_UP>
+template <typename XT, bool GATE_UP>
 void launch_experts(l4moe_elem type, dim3 grid, cudaStream_t st, const GroupTable* tab, int E, int group,
                     const mv::Experts& ptrs, const mv::Rows& rows) {
-    if (type == L4MOE_ELEM_F32) launch_experts_t<float, GATE_UP>(grid, st, tab, E, group, ptrs, rows);
-    else if (type == L4MOE_ELEM_BF16) launch_experts_t<__nv_bfloat16, GATE_UP>(grid, st, tab, E, group, ptrs, rows);
-    else launch_experts_t<__half, GATE_UP>(grid, st, tab, E, group, ptrs, rows);
+    if (type == L4MOE_ELEM_F32) launch_experts_t<XT, float, GATE_UP>(grid, st, tab, E, group, ptrs, rows);
+    else if (type == L4MOE_ELEM_BF16)
+        launch_experts_t<XT, __nv_bfloat16, GATE_UP>(grid, st, tab, E, group, ptrs, rows);
+    else launch_experts_t<XT, __half, GATE_UP>(grid, st, tab, E, group, ptrs, rows);
 }
 
 // The launch sequence of one forward.  w / ws_tokens: the workspace and the
@@ -593,7 +595,20 @@ l4moe_status run_layer(l4moe_handle* h, int T, const void* x, const void* Wr, co
     // split-K k-ranges when a small batch leaves too few tiles
     const SplitPlan plan = split_plan(p, T, h->sms, h->top_k, ACT8);
     const int s_gu = plan.s_gu, s_dn = plan.s_dn;
-    if (E > 0 && T <= kSmallMaxTokens) {
+    // experts with group scales, a few tokens: routing without row copies
+    // (the products gather their bf16 rows themselves)
+    const bool gather = grouped && E > 0 && T <= rg::kTokens && E % 8 == 0;
+    if (gather) {
+        static std::atomic<uint64_t> attr_done{0};
+        ensure_smem_attr(attr_done, rg::route_group_kernel, rg::smem_bytes());
+        LaunchTimer t_router(h, 0, st);
+        launch_cluster_x(rg::route_group_kernel, dim3(rg::kCtas), dim3(rg::kThreads), rg::smem_bytes(), st,
+                         (unsigned)rg::kCtas, static_cast<const __nv_bfloat16*>(x),
+                         static_cast<const __nv_bfloat16*>(Wr), (const float*)h->bias, T, d, E, k, idx, gate, lmax,
+                         margin, counts, offsets, perm, gslot, tab_gu);
+        t_router.stop();
+        L4MOE_CHECK_LAUNCH("grouped routing launch");
+    } else if (E > 0 && T <= kSmallMaxTokens) {
         // a few tokens: router, top-k, permutation and row copy in one launch
         const int slices = (d + kSmallSliceK - 1) / kSmallSliceK;
         float* part_logits = reinterpret_cast<float*>(w + L.logits);
@@ -716,10 +731,15 @@ l4moe_status run_layer(l4moe_handle* h, int T, const void* x, const void* Wr, co
             // 8 rows, the sums of a token added by the down finish
             const bool has = E > 0;
             mv::Rows R{};
-            R.x[0] = xg, R.x[1] = x16;
+            R.x[0] = gather ? x : (const void*)xg;
+            R.x[1] = gather ? x : (const void*)x16;
+            R.gather = gather;
+            R.perm = perm;
+            R.k = k;
+            R.shared_rows = gather ? T : 0;
             R.K[0] = R.K[1] = d;
             R.N[0] = 2 * F, R.N[1] = 2 * Fs;
-            R.scale[0] = gslot, R.scale[1] = tokscale;
+            R.scale[0] = gslot, R.scale[1] = gather ? nullptr : tokscale;
             R.h[0] = hr, R.h[1] = hs;
             R.err = err;
             mv::Experts ptrs;
@@ -740,7 +760,9 @@ l4moe_status run_layer(l4moe_handle* h, int T, const void* x, const void* Wr, co
             fill(grouped->gate_up, grouped->shared_gate_up, 0);
             {
                 LaunchTimer t_gu(h, 3, st);
-                launch_experts<true>(h->group_type, dim3(gt, units, sg), st, tab_gu, E, h->group, ptrs, R);
+                const dim3 grid(gt, units, sg);
+                if (gather) launch_experts<__nv_bfloat16, true>(h->group_type, grid, st, tab_gu, E, h->group, ptrs, R);
+                else launch_experts<__half, true>(h->group_type, grid, st, tab_gu, E, h->group, ptrs, R);
                 t_gu.stop();
                 L4MOE_CHECK_LAUNCH("grouped gate/up launch");
             }
@@ -750,9 +772,9 @@ l4moe_status run_layer(l4moe_handle* h, int T, const void* x, const void* Wr, co
             R.K[0] = F, R.K[1] = Fs;
             R.N[0] = R.N[1] = d;
             R.part[0] = part, R.part[1] = part + (size_t)(has ? Tv : 0) * d;
-            R.perm = perm;
             LaunchTimer t_dn(h, 4, st);
-            launch_experts<false>(h->group_type, dim3(dt, units, sd), st, tab_dn, E, h->group, ptrs, R);
+            launch_experts<__half, false>(h->group_type, dim3(dt, units, sd), st, gather ? tab_gu : tab_dn, E,
+                                          h->group, ptrs, R);
             L4MOE_CHECK_LAUNCH("grouped down launch");
             const long long n = (long long)T * d;
             launch_k(down_finish_kernel<ET>, dim3((int)std::min<long long>((n / 4 + 255) / 256, 8LL * h->sms)),
