@@ -6,7 +6,6 @@ if the compiled library is missing or the call fails, an exception is raised.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -128,9 +127,17 @@ def _ptr_array(tensors):
     return arr
 
 
+# The current stream's raw handle and the current device without the Stream
+# object and the index parsing of torch.cuda.current_stream(), which cost more
+# than a small kernel's launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream_handle(stream) -> int | None:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _raw_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -170,26 +177,49 @@ def check_op(st: int):
         raise L4MoEError(st, load_library().l4moe_last_error(None).decode())
 
 
-@contextlib.contextmanager
+class _Elsewhere:
+    """Runs an operator on another device or stream than the current ones:
+    both are current inside, so buffers allocated there belong to the stream
+    that uses them."""
+
+    def __init__(self, device, stream):
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        if stream is not None and stream.device != device:
+            raise ValueError(f"l4moe: stream of {stream.device}, tensors on {device}")
+        self._scope = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
+        self._device, self._stream = device, stream
+
+    def __enter__(self):
+        self._scope.__enter__()
+        return (self._stream or torch.cuda.current_stream(self._device)).cuda_stream
+
+    def __exit__(self, *exc):
+        return self._scope.__exit__(*exc)
+
+
+class _Here:
+    """The current device and stream (the usual call, kept cheap)."""
+
+    def __init__(self, handle):
+        self._handle = handle
+
+    def __enter__(self):
+        return self._handle
+
+    def __exit__(self, *exc):
+        return None
+
+
 def op_stream(tensor, stream):
-    """Run one operator on `tensor`'s device and on `stream` (a torch stream
-    or a raw handle; None: that device's current one): both are current
-    inside, so buffers allocated there belong to the stream that uses them.
-    Yields the raw handle."""
-    dev = tensor.device
+    """Context of one operator call on `tensor`'s device and on `stream` (a
+    torch stream or a raw handle; None: that device's current one).  Gives the
+    raw handle."""
     if stream is None:
-        if dev.index == torch.cuda.current_device():
-            yield torch.cuda.current_stream(dev).cuda_stream
-        else:
-            with torch.cuda.device(dev):
-                yield torch.cuda.current_stream(dev).cuda_stream
-        return
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=dev)
-    if stream.device != dev:
-        raise ValueError(f"l4moe: stream of {stream.device}, tensors on {dev}")
-    with torch.cuda.stream(stream):
-        yield stream.cuda_stream
+        index = tensor.get_device()
+        if index == _current_device():
+            return _Here(_raw_stream(index))
+    return _Elsewhere(tensor.device, stream)
 
 
 class _DevView:
@@ -355,10 +385,10 @@ class L4MoE:
 
     def _forward_bound(self, x, bound, out, stream):
         T = self._check_io(x, bound.W_router, out)
-        if x.device != self.device or (out is not None and out.device != self.device):
+        if x.get_device() != self.device.index or (out is not None and out.get_device() != self.device.index):
             raise ValueError(f"l4moe: x or out is not on the layer's device {self.device}")
         if out is None:
-            out = torch.empty((T, self.d_model), dtype=x.dtype, device=x.device)
+            out = x.new_empty((T, self.d_model))
         gu, dn = bound.arrays
         self._check(self._lib.l4moe_forward(self._h, T, _ptr(x), bound.router_ptr, gu, dn, bound.shared[0],
                                             bound.shared[1], _ptr(out), _stream_handle(stream)))

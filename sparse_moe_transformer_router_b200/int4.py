@@ -21,7 +21,8 @@ MAX_TOKENS = 64
 _X_TYPES = (torch.bfloat16, torch.float16)
 
 
-def _check(x, w, scales, group, out):
+def _refuse(x, w, scales, group, out):
+    """Name what is wrong with a call that `_shapes` did not accept."""
     if x.dim() != 2 or w.dim() != 2 or scales.dim() != 2:
         raise ValueError("l4moe: x [T, K], w [K, N / 2] and scales [ceil(K / group), N] are matrices")
     T, K = x.shape
@@ -53,17 +54,44 @@ def _check(x, w, scales, group, out):
             raise ValueError(f"l4moe: {name} is on {t.device}, x on {x.device}")
     if torch.is_grad_enabled() and (x.requires_grad or scales.requires_grad):
         raise ValueError("l4moe: int4_matvec has no gradient; call it under torch.no_grad() or detach x and scales")
-    return T, K, N
+
+
+def _accepts(x, w, scales, group, out, T, K, N):
+    """The conditions of `_refuse` in one pass (a call of a few microseconds
+    pays for every look at a tensor)."""
+    dev = x.get_device()
+    return (x.dtype in _X_TYPES and w.dtype is torch.uint8 and scales.dtype in ELEMS and group >= 32
+            and group % 32 == 0 and T <= MAX_TOKENS and K >= 1 and N >= 2 and w.shape == (K, N // 2)
+            and scales.shape == (-(-K // group), N) and dev >= 0 and w.get_device() == dev
+            and scales.get_device() == dev and x.is_contiguous() and w.is_contiguous() and scales.is_contiguous()
+            and (out is None or (out.shape == (T, N) and out.dtype is x.dtype and out.get_device() == dev
+                                 and out.is_contiguous()))
+            and not ((x.requires_grad or scales.requires_grad) and torch.is_grad_enabled()))
 
 
 def int4_matvec(x: torch.Tensor, w: torch.Tensor, scales: torch.Tensor, group: int, out: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
     """x [T, K] times the 4-bit weight w with group scales: [T, N] in x's type."""
     group = int(group)
-    T, K, N = _check(x, w, scales, group, out)
+    if x.dim() != 2 or w.dim() != 2 or scales.dim() != 2:
+        _refuse(x, w, scales, group, out)
+    (T, K), N = x.shape, 2 * w.shape[1]
+    if not _accepts(x, w, scales, group, out, T, K, N):
+        _refuse(x, w, scales, group, out)
+        raise ValueError("l4moe: int4_matvec does not take these arguments")
     with op_stream(x, stream) as st:
         if out is None:
-            out = torch.empty((T, N), dtype=x.dtype, device=x.device)
-        check_op(load_library().l4moe_int4_matvec(T, K, N, group, x.data_ptr(), ELEMS[x.dtype], w.data_ptr(),
-                                                  scales.data_ptr(), ELEMS[scales.dtype], out.data_ptr(), st))
+            out = x.new_empty((T, N))
+        check_op(_call()(T, K, N, group, x.data_ptr(), ELEMS[x.dtype], w.data_ptr(), scales.data_ptr(),
+                         ELEMS[scales.dtype], out.data_ptr(), st))
     return out
+
+
+_function = None
+
+
+def _call():
+    global _function
+    if _function is None:
+        _function = load_library().l4moe_int4_matvec
+    return _function

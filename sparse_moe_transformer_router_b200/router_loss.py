@@ -27,6 +27,8 @@ caller's stream, with no host synchronisation.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from .binding import ELEMS, check_op, load_library, op_stream
@@ -36,7 +38,24 @@ MAX_EXPERTS = 256
 MAX_K = 4
 
 
-def _check(logits, k, score, mask, idx):
+def _accepts(logits, k, score, mask, idx):
+    """The conditions of `_refuse` in one pass (a call of a few microseconds
+    pays for every look at a tensor)."""
+    if logits.dim() != 2:
+        return False
+    T, E = logits.shape
+    dev = logits.get_device()
+    return (logits.dtype in ELEMS and 1 <= E <= MAX_EXPERTS and 1 <= k <= MAX_K and k <= E and score in SCORES
+            and dev >= 0 and logits.is_contiguous()
+            and (mask is None or (mask.shape == (T,) and mask.dtype is torch.bool and mask.get_device() == dev
+                                  and mask.is_contiguous()))
+            and (idx is None or (idx.shape == (T, k) and idx.dtype is torch.int32 and idx.get_device() == dev
+                                 and idx.is_contiguous())))
+
+
+def _refuse(logits, k, score, mask, idx):
+    """Name what is wrong with a call (the rarer good ones pass: row strides,
+    a flat idx)."""
     if logits.dim() != 2:
         raise ValueError(f"l4moe: logits must be [T, E], got shape {tuple(logits.shape)}")
     T, E = logits.shape
@@ -80,28 +99,11 @@ class RouterLoss:
 
     def __init__(self, logits, mask, score, result):
         self._logits, self._mask, self._score, self._result = logits, mask, score, result
-        self._loss = None  # the loss with its autograd history
-
-    @property
-    def loss(self) -> torch.Tensor:
-        return self._result[0] if self._loss is None else self._loss
-
-    @property
-    def balance(self) -> torch.Tensor:
-        return self._result[1]
-
-    @property
-    def z(self) -> torch.Tensor:
-        return self._result[2]
-
-    @property
-    def rows(self) -> torch.Tensor:
-        return self._result[3]
+        self.loss, self.balance, self.z, self.rows = result[:4].unbind()
 
     @property
     def counts(self) -> torch.Tensor:
-        E = self._logits.shape[1]
-        return self._result[4:4 + E].view(torch.int32)
+        return self._result.view(torch.int32)[4:4 + self._logits.shape[1]]
 
     def grad(self, upstream: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """The gradient of the logits, times `upstream` (an fp32 device
@@ -110,7 +112,8 @@ class RouterLoss:
         logits = self._logits
         T, E = logits.shape
         if upstream is not None:
-            if upstream.dtype != torch.float32 or upstream.numel() != 1 or upstream.device != logits.device:
+            if upstream.dtype is not torch.float32 or upstream.numel() != 1 or \
+                    upstream.get_device() != logits.get_device():
                 raise ValueError("l4moe: upstream must be one float32 on the logits' device")
         if out is not None:
             if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
@@ -118,7 +121,7 @@ class RouterLoss:
             _rows(out, "out")
         with op_stream(logits, stream) as st:
             if out is None:
-                out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+                out = logits.new_empty((T, E))
             check_op(load_library().l4moe_router_loss_grad(
                 T, E, logits.data_ptr(), ELEMS[logits.dtype], _stride(logits),
                 None if self._mask is None else self._mask.data_ptr(), self._score, self._result.data_ptr(),
@@ -126,14 +129,20 @@ class RouterLoss:
         return out
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace(T, E, device) -> int:
+    """l4moe_router_loss_workspace on the current device (`device`)."""
+    return load_library().l4moe_router_loss_workspace(T, E)
+
+
 def _forward(logits, k, balance, z, score, mask, idx, stream) -> RouterLoss:
     lib = load_library()
     T, E = logits.shape
     with op_stream(logits, stream) as st:
-        n = lib.l4moe_router_loss_workspace(T, E)
+        n = _workspace(T, E, logits.get_device())
         words = 4 + 2 * E + 1
         # one buffer: the result, then the workspace
-        buf = torch.empty(words + n // 4, dtype=torch.float32, device=logits.device)
+        buf = logits.new_empty(words + n // 4, dtype=torch.float32)
         at = buf.data_ptr()
         check_op(lib.l4moe_router_loss(
             T, E, k, logits.data_ptr(), ELEMS[logits.dtype], _stride(logits), None if mask is None else mask.data_ptr(),
@@ -150,7 +159,7 @@ class _Loss(torch.autograd.Function):
         box.append(r)
         ctx.save_for_backward(logits, r._result)
         ctx.mask, ctx.score = r._mask, r._score
-        return r._result[0].clone()
+        return r.loss.clone()
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -169,12 +178,13 @@ def router_loss(logits: torch.Tensor, k: int = 1, *, balance: float = 1e-2, z: f
     choices (None: each row's k largest logits).  balance and z are the
     weights of the two losses in `loss`."""
     k = int(k)
-    _check(logits, k, score, mask, idx)
+    if not _accepts(logits, k, score, mask, idx):
+        _refuse(logits, k, score, mask, idx)
     args = (k, float(balance), float(z), score, mask, idx, stream)
     if not (logits.requires_grad and torch.is_grad_enabled()):
         return _forward(logits, *args)
     box = []
     loss = _Loss.apply(logits, args, box)
     r = box[0]
-    r._loss = loss
+    r.loss = loss
     return r
