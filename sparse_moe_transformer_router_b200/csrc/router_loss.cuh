@@ -461,7 +461,7 @@ __device__ __forceinline__ void cluster_result(const float* P, const int* c, con
 // first block adds the others' sums, over distributed shared memory, and
 // writes the result; more blocks leave partials for the finishing kernel.
 template <typename IT, int L, bool SIG>
-__global__ void __launch_bounds__(kLossThreads) router_loss_kernel(
+__global__ void __launch_bounds__(kLossThreads, 2) router_loss_kernel(
     const IT* __restrict__ logits, long long ld, int T, int E, int k, int vec, const uint8_t* __restrict__ mask,
     const int32_t* __restrict__ idx, float wb, float wz, float* __restrict__ part, float* __restrict__ result) {
     op::pdl_enter();
