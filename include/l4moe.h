@@ -413,7 +413,7 @@ L4MOE_API l4moe_status l4moe_router_loss_grad(int T, int E, const void *logits, 
  * even column in the low one); scales [ceil(K / group), N] of s_type; group a
  * multiple of 32 (group >= K: one scale per column; the last group may be
  * short).  Any 1 <= K <= 2^30 and even
- * 2 <= N <= 2^30; rows of a multiple of 32 columns are read
+ * 2 <= N <= 2^30; K a multiple of 8 and N of 32 are read
  * in wide loads.  Sums are fp32 and the result is rounded once.  Every f16 x
  * is taken exactly; bf16 rows are divided by a power of two into f16's range,
  * exact down to 2^-31 of the row's largest magnitude and to 2^-39 of it

@@ -6,6 +6,7 @@
 #include "int4_mv.cuh"
 #include "l4moe.h"
 #include "launch.cuh"
+#include "tensor_map.cuh"
 
 using namespace l4moe;
 
@@ -17,26 +18,39 @@ struct Call {
     const uint8_t* w;
     void* y;
     cudaStream_t st;
-    bool vec;
+    bool tma;
 };
 
-template <int NT8, typename XT, typename ST, bool VEC>
+template <typename T>
+constexpr CUtensorMapDataType map_type() {
+    return std::is_same<T, float>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+           : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+
+template <int NT8, typename XT, typename ST, bool TMA>
 cudaError_t launch(const Call& c) {
-    constexpr size_t smem = mv::Cfg<NT8, ST>::SMEM;
+    using Cf = mv::Cfg<NT8, ST>;
     static std::atomic<uint64_t> attr_done{0};
-    ensure_smem_attr(attr_done, mv::int4_matvec_kernel<NT8, XT, ST, VEC>, smem);
+    ensure_smem_attr(attr_done, mv::int4_matvec_kernel<NT8, XT, ST, TMA>, Cf::SMEM);
     const int tiles = (c.N + mv::kCols - 1) / mv::kCols, tt = (c.T + NT8 * 8 - 1) / (NT8 * 8);
-    const int S = mv::slices((long long)tiles * tt, c.K, c.sms, mv::Cfg<NT8, ST>::PER_SM);
-    const mv::Weight<ST> W{c.w, static_cast<const ST*>(c.s), c.N / 2, c.N, c.K, c.group};
-    launch_kc(mv::int4_matvec_kernel<NT8, XT, ST, VEC>, dim3(tiles, tt, S), dim3(mv::kThreads), smem, c.st,
-              S > 1 ? (unsigned)S : 0u, static_cast<const XT*>(c.x), c.T, W, static_cast<XT*>(c.y));
+    const int S = mv::slices((long long)tiles * tt, c.K, c.sms, Cf::PER_SM);
+    CUtensorMap qm{}, sm{}, xm{};
+    if (TMA && (!encode_2d(&qm, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.w, (uint64_t)c.N / 2, (uint64_t)c.K,
+                           (uint64_t)c.N / 2, 64, mv::kRows, CU_TENSOR_MAP_SWIZZLE_64B) ||
+                !encode_2d(&sm, map_type<ST>(), c.s, (uint64_t)c.N, ((uint64_t)c.K + c.group - 1) / c.group,
+                           (uint64_t)c.N * sizeof(ST), mv::kCols, 1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+                !encode_2d(&xm, map_type<XT>(), c.x, (uint64_t)c.K, (uint64_t)c.T, (uint64_t)c.K * 2, mv::kRows, 1)))
+        return cudaErrorInvalidValue;
+    const mv::Weight<ST> W{nullptr, nullptr, c.w, static_cast<const ST*>(c.s), c.N, c.K, c.group};
+    launch_kc(mv::int4_matvec_kernel<NT8, XT, ST, TMA>, dim3(tiles, tt, S), dim3(mv::kThreads), Cf::SMEM, c.st,
+              S > 1 ? (unsigned)S : 0u, qm, sm, xm, static_cast<const XT*>(c.x), c.T, W, static_cast<XT*>(c.y));
     return cudaGetLastError();
 }
 
 template <typename XT, typename ST>
 cudaError_t launch_x(const Call& c) {
-    if (c.T <= 8) return c.vec ? launch<1, XT, ST, true>(c) : launch<1, XT, ST, false>(c);
-    return c.vec ? launch<2, XT, ST, true>(c) : launch<2, XT, ST, false>(c);
+    if (c.T <= 8) return c.tma ? launch<1, XT, ST, true>(c) : launch<1, XT, ST, false>(c);
+    return c.tma ? launch<2, XT, ST, true>(c) : launch<2, XT, ST, false>(c);
 }
 
 template <typename XT>
@@ -70,9 +84,9 @@ extern "C" l4moe_status l4moe_int4_matvec(int T, int K, int N, int group, const 
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return op_fail(L4MOE_ERR_CUDA, "l4moe_int4_matvec: no CUDA device");
-    // 16-byte copies when every row starts on 16 bytes
+    // tensor maps want rows that start on 16 bytes
     const Call c{T, K, N, group, sms, x, scales, static_cast<const uint8_t*>(w), y,
-                 static_cast<cudaStream_t>(stream), N % 32 == 0};
+                 static_cast<cudaStream_t>(stream), N % 32 == 0 && K % 8 == 0};
     const cudaError_t e =
         x_type == L4MOE_ELEM_BF16 ? launch_s<__nv_bfloat16>(c, s_type) : launch_s<__half>(c, s_type);
     if (e == cudaSuccess) return L4MOE_OK;

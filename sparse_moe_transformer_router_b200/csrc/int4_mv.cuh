@@ -16,9 +16,12 @@
 //   to 8 tokens as the 8 columns.  tcgen05 would take its weight operand from
 //   shared memory, a round trip for widened weights that nothing is gained
 //   from at 8 columns.
-// - A warp takes blocks of 32 rows by 128 columns through a ring of its own
-//   in shared memory, filled by asynchronous 16-byte copies.  The operand
-//   wants pairs along K: a transposing matrix load of 16-bit units, four
+// - A warp takes 128 columns by 64 rows at a time through a ring of its own in
+//   shared memory, filled by TMA: one lane's few instructions bring the
+//   weight's box, the scales of the groups that begin there and the tokens'
+//   rows.  (As cp.async by every lane the copies cost as many issue slots as a
+//   third of the arithmetic: 113 us for 5120 x 202048 against what is noted
+//   below.)  The operand wants pairs along K: a transposing matrix load of 16-bit units, four
 //   columns each, returns two rows' units in one register.  Each pair of
 //   nibbles is then one AND (with the sign bit flipped) away: u = q + 8 in
 //   [0, 15] left where it lies in the f16's low bits is the subnormal u 2^-24
@@ -34,14 +37,18 @@
 //   (exact for values down to 2^-31 of it, others round at 2^-39 of it).
 //   A row with an infinity or a NaN gives NaN (inf times the bias).
 //
-// A CTA of four warps takes 128 columns and a slice of K, each warp a quarter
-// of the slice; the quarters are added through shared memory and the slices
-// of a cluster through distributed shared memory, always in the same order.
+// A CTA has four warps.  As an operator (and for the down product) it takes
+// 128 columns and a slice of K, each warp a quarter of the slice; for gate/up
+// it takes the 128 gate columns and the 128 up columns of the same hidden
+// values, each by two warps with half of the slice.  The warps' sums are added
+// through shared memory and the slices of a cluster through distributed shared
+// memory, always in the same order.  Every wait for a copy gives up after a
+// second: the sums become NaN (and the layer's error word gets a bit).
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
-#include <cstring>
 #include <type_traits>
 
 #include "schedule.cuh"
@@ -50,28 +57,29 @@
 namespace l4moe {
 namespace mv {
 
-constexpr unsigned kErrF16Range = 1u << 4;  // DEV_ERR_F16_RANGE of the layer's error word
+constexpr unsigned kErrTimeout = 1u << 0;   // DEV_ERR_TIMEOUT_PRODUCER of the layer's error word
+constexpr unsigned kErrF16Range = 1u << 4;  // DEV_ERR_F16_RANGE
 
-constexpr int kWarps = 4;        // of a CTA, each on a quarter of the CTA's slice of K
+constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kCols = 128;       // columns of a CTA: two halves of 64
-constexpr int kHalf = kCols / 2;
-constexpr int kBlock = 32;       // rows of a block (scale groups are multiples of it)
+constexpr int kCols = 128;       // columns of a warp
+constexpr int kBlock = 32;       // rows that share a scale at least (scale groups are multiples of it)
+constexpr int kRows = 64;        // rows of a stage
+constexpr int kXRow = 2 * kRows; // bytes of a token's row in a stage
 
-// A warp's ring of blocks: 32 rows of 64 bytes of the weight, the scales of
-// the columns, 64 bytes (32 rows) of each token.
+// A warp's ring.  Stage: the weight's 64 rows of 64 bytes, the tokens' 64
+// values, two rows of scales (of the group of each 32 rows, where it begins).
 template <int NT8, typename ST>
 struct Cfg {
-    static constexpr int WORDS = kBlock * 64;
-    static constexpr int XOFF = WORDS + kCols * (int)sizeof(ST);
-    static constexpr int STAGE = XOFF + NT8 * 8 * 64;
-    static constexpr int STAGES = 4;
+    static constexpr int XOFF = kRows * 64;
+    static constexpr int SOFF = XOFF + NT8 * 8 * kXRow;
+    static constexpr int STAGE = (SOFF + 2 * kCols * (int)sizeof(ST) + 1023) / 1024 * 1024;  // the swizzles' period
+    // three CTAs share an SM (168 registers a thread)
+    static constexpr int PER_SM = 3;
+    static constexpr int STAGES = NT8 == 1 ? 3 : 2;
     static constexpr int RING = STAGES * STAGE;
-    // CTAs that share an SM: the registers' limit (up to 8 tokens 128 a
-    // thread, 16 tokens 168)
-    static constexpr int PER_SM = NT8 == 1 ? 4 : 3;
-    static constexpr int RED = (int)sizeof(float) * kWarps * NT8 * 8 * kCols;  // over all of it
-    static constexpr int SMEM = kWarps * RING > RED ? kWarps * RING : RED;
+    static constexpr int RED = (int)sizeof(float) * kWarps * NT8 * 8 * kCols;  // over the rings
+    static constexpr int SMEM = (kWarps * RING > RED ? kWarps * RING : RED) + 1024;  // and room to align them
 };
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
@@ -98,168 +106,35 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t mask, uint32_t 
     return r;
 }
 
-// A weight matrix as a warp sees it.
+// A weight matrix: its codes and scales behind tensor maps (boxes of 64 rows by
+// 64 bytes and of one row by 128 columns), or, for sizes that those do not
+// take, in memory.
 template <typename ST>
 struct Weight {
-    const uint8_t* q;      // [K, row_bytes]
+    const CUtensorMap *qm, *sm;
+    const uint8_t* q;      // [K, N / 2]
     const ST* s;           // [groups, N]
-    long long row_bytes;   // N / 2
-    int N;                 // columns of a row of scales
-    int K, group;
+    int N, K, group;
 };
 
-// Where a stage holds the 16 bytes of columns 32 c .. 32 c + 31 of row r (or of
-// rows 8 c .. 8 c + 7 of token r): the eight rows of a matrix load lie in
-// different banks.
+// Where a stage holds the 16 bytes of columns 32 c .. 32 c + 31 of row r, and
+// values 8 c .. 8 c + 7 of token t (TMA's 64- and 128-byte swizzles): the
+// eight rows of a matrix load lie in different banks.
 __device__ __forceinline__ constexpr int chunk_at(int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); }
-
-// The 128 columns of a CTA: two runs of 64, each with the first column that
-// does not exist.
-struct Columns {
-    int col0, col1, limit0, limit1;
-    __device__ __forceinline__ int first(int second) const { return second ? col1 : col0; }
-    __device__ __forceinline__ int end(int second) const { return second ? limit1 : limit0; }
-};
-
-// A weight matrix's blocks as one lane loads them.  VEC (rows of a multiple
-// of 32 columns): asynchronous 16-byte copies, lane l 16 bytes of rows l / 4,
-// l / 4 + 8, ... and its four columns' scales; else plain loads, byte by
-// byte.  What lies past K or past the columns' limit is not loaded: x is zero
-// there and such columns are not stored, and no nibble is an infinity or a
-// NaN.
-template <typename ST, bool VEC>
-struct Loader {
-    const uint8_t* q;     // VEC: this lane's 16 bytes of its first row; else this lane's row
-    const ST* s;          // VEC: this lane's 4 scales of the next block; else the row of scales
-    long long row_bytes;
-    int N, group;
-    int left;             // rows until the next group
-    int rows;             // rows of K left from the next block on
-    bool in, in_s;        // VEC: this lane's columns exist
-
-    __device__ __forceinline__ void start(const Weight<ST>& W, const Columns& C, int row, int lane) {
-        row_bytes = W.row_bytes, N = W.N, group = W.group;
-        const int grp = row / group;
-        left = 0;
-        first = group - (row - grp * group);
-        rows = W.K - row;
-        s = W.s + (long long)grp * N;
-        if constexpr (VEC) {
-            const int col = C.first(lane & 2) + (lane & 1) * 32;
-            in = col < C.end(lane & 2);
-            q = W.q + (long long)(row + (lane >> 2)) * row_bytes + (col >> 1);
-            const int cs = C.first(lane & 16) + (lane & 15) * 4;
-            in_s = cs < C.end(lane & 16);
-            s += cs;
-        } else {
-            q = W.q + (long long)(row + lane) * row_bytes;
-        }
-    }
-    int first;            // rows until the first change of group
-    __device__ __forceinline__ void issue(uint32_t stage, uint8_t* generic, const Columns& C, int lane) {
-        constexpr int WORDS = Cfg<1, ST>::WORDS;
-        const bool fresh = left == 0;  // this warp's first block of its group: its scales too
-        if constexpr (VEC) {
-            const uint32_t dst = stage + chunk_at(lane >> 2, lane & 3);
-            const long long step = 8 * row_bytes;
-            const uint8_t *p1 = q + step, *p2 = p1 + step, *p3 = p2 + step;
-            if (in) {
-                if (rows >= kBlock) {
-                    op::cp_async<16>(dst, q);
-                    op::cp_async<16>(dst + 512, p1);
-                    op::cp_async<16>(dst + 1024, p2);
-                    op::cp_async<16>(dst + 1536, p3);
-                } else {
-                    const int n = rows - (lane >> 2);
-                    if (n > 0) op::cp_async<16>(dst, q);
-                    if (n > 8) op::cp_async<16>(dst + 512, p1);
-                    if (n > 16) op::cp_async<16>(dst + 1024, p2);
-                    if (n > 24) op::cp_async<16>(dst + 1536, p3);
-                }
-            }
-            q = p3 + step;
-            if (fresh && in_s) op::cp_async<4 * (int)sizeof(ST)>(stage + WORDS + lane * 4 * (int)sizeof(ST), s);
-        } else {
-            if (lane < rows) {  // the 64 bytes of the lane's row; col and limit are even: whole bytes
-                for (int c = 0; c < 4; ++c) {
-                    const int col = C.first(c & 2) + (c & 1) * 32;
-                    const int nb = min(16, (C.end(c & 2) - col) >> 1);
-                    const uint8_t* p = q + (col >> 1);
-                    uint32_t v[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-                    for (int b = 0; b < 16; ++b)
-                        if (b < nb) v[b >> 2] |= (uint32_t)__ldg(p + b) << (8 * (b & 3));
-                    *reinterpret_cast<uint4*>(generic + chunk_at(lane, c)) = make_uint4(v[0], v[1], v[2], v[3]);
-                }
-            }
-            q += kBlock * row_bytes;
-            ST* d = reinterpret_cast<ST*>(generic + WORDS) + lane * 4;
-            const int cs = C.first(lane & 16) + (lane & 15) * 4;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (fresh && cs + j < C.end(lane & 16)) d[j] = s[cs + j];
-        }
-        rows -= kBlock;
-        if (fresh) left = first, first = group;
-        left -= kBlock;
-        if (left == 0) s += N;
-    }
-};
+__device__ __forceinline__ constexpr int token_at(int t, int c) { return t * kXRow + ((c ^ (t & 7)) << 4); }
 
 // The token rows of a CTA: rows of x, ld apart, from row0 on, or those that
 // slot row0 + token of perm names (entry / k).
 template <typename XT>
 struct Tokens {
+    const CUtensorMap* map;  // boxes of one row by 64 values
     const XT* x;
     long long ld;
     int row0;
     const int32_t* perm;
     int k;
-    __device__ __forceinline__ const XT* row(int token) const {
-        const int r = perm ? perm[row0 + token] / k : row0 + token;
-        return x + r * ld;
-    }
-};
-
-// The tokens' rows as one lane loads them: 8 values (16 bytes) of tokens
-// l / 4, l / 4 + 8.  Rows past the slice's end are zeros; tokens past nt are
-// not loaded (a token is a column of the products, and what such a column
-// holds reaches no other).
-template <int NT8, typename XT>
-struct XLoader {
-    const XT* x[NT8];  // this lane's 8 values of tokens l / 4, l / 4 + 8 in the next block
-    int rows;          // rows left from this lane's on
-    bool vec;          // rows (and so 8 values) start on 16 bytes
-
-    __device__ __forceinline__ void start(const Tokens<XT>& X, int nt, int row, int end, int lane) {
-        vec = (X.ld & 7) == 0;
-#pragma unroll
-        for (int n = 0; n < NT8; ++n) {
-            const int tok = n * 8 + (lane >> 2);
-            x[n] = X.row(tok < nt ? tok : 0) + row + (lane & 3) * 8;
-        }
-        rows = end - row - (lane & 3) * 8;
-    }
-    __device__ __forceinline__ void issue(uint32_t at, uint8_t* generic, int nt, int lane) {
-#pragma unroll
-        for (int n = 0; n < NT8; ++n) {
-            const int off = n * 8 * 64 + chunk_at(lane >> 2, lane & 3);
-            if ((lane >> 2) + 8 * n < nt) {
-                const XT* p = x[n];
-                if (vec) {
-                    op::cp_async16_zero(at + off, p, rows > 0);  // 8 values or none: rows of a multiple of 8
-                } else {
-                    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < rows) w[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[j] << (16 * (j & 1));
-                    *reinterpret_cast<uint4*>(generic + off) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
-            x[n] += kBlock;
-        }
-        rows -= kBlock;
-    }
+    __device__ __forceinline__ int at(int token) const { return perm ? perm[row0 + token] / k : row0 + token; }
+    __device__ __forceinline__ const XT* row(int token) const { return x + at(token) * ld; }
 };
 
 // Column (of the warp's 128) that accumulator tile i of lane group g holds in
@@ -267,7 +142,7 @@ struct XLoader {
 // tiles hold 16 times their sum.
 __device__ __forceinline__ constexpr int tile_col(int i, int g) { return (i >> 1) * 32 + 4 * g + (i & 1); }
 
-// acc += one block: the warp's stage (rows_at: this lane's address of a matrix
+// acc += 32 rows of the warp's stage (rows_at: this lane's address of a matrix
 // load of the weight, x_at: of the tokens); sc: the scales of the lane's
 // columns; f: what the lane's tokens (column l / 4 of each 8) are multiplied
 // with as they become f16.  b8 += -8 2^-24 sum(x) of the lane's two tokens: a
@@ -279,7 +154,7 @@ __device__ __forceinline__ void block_fma(float (&acc)[NT8][8][4], float (&b8)[N
     uint32_t b[NT8][4];
 #pragma unroll
     for (int n = 0; n < NT8; ++n) {
-        op::ldmatrix(b[n], x_at + n * 8 * 64);
+        op::ldmatrix(b[n], x_at + n * 8 * kXRow);
         if constexpr (BF) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -409,36 +284,121 @@ __device__ __forceinline__ float find_factors(const Tokens<__nv_bfloat16>& X, in
     return mine;
 }
 
-// The sums of this CTA's slice [k0, k1) of K, left in smem as [token][128
-// columns] fp32 for the nt tokens.  tokens(): the token rows, asked for once
-// the first weight loads are on their way.
-template <int NT8, typename XT, typename ST, bool VEC, typename F>
-__device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, const Columns& C, int nt, int k0, int k1,
-                                           F&& tokens) {
+// One stage's plain loads, for sizes that tensor maps do not take: lane l rows
+// l and l + 32 of the weight byte by byte, tokens and scales element by
+// element, zeros where nothing is (scales past N are not written: such
+// columns are not stored).
+template <int NT8, typename XT, typename ST>
+__device__ __forceinline__ void load_plain(uint8_t* stage, const Weight<ST>& W, int col0, const Tokens<XT>& X, int nt,
+                                           int row, int end, bool s0, bool s1, int grp, int lane) {
+    using Cf = Cfg<NT8, ST>;
+    const int nb = min(64, (W.N - col0) >> 1);  // N is even: whole bytes
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = lane + 32 * h;
+        const uint8_t* p = W.q + (long long)(row + r) * (W.N / 2) + (col0 >> 1);
+        for (int c = 0; c < 4; ++c) {
+            uint32_t v[4] = {0u, 0u, 0u, 0u};
+            if (row + r < W.K) {
+#pragma unroll
+                for (int b = 0; b < 16; ++b)
+                    if (c * 16 + b < nb) v[b >> 2] |= (uint32_t)__ldg(p + c * 16 + b) << (8 * (b & 3));
+            }
+            *reinterpret_cast<uint4*>(stage + chunk_at(r, c)) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    }
+    for (int i = lane; i < nt * 8; i += 32) {
+        const int t = i >> 3, c = i & 7;
+        *reinterpret_cast<uint4*>(stage + Cf::XOFF + token_at(t, c)) =
+            load_x8(X.row(t) + row, c * 8, end - row, false);
+    }
+    ST* d = reinterpret_cast<ST*>(stage + Cf::SOFF);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (h ? !s1 : !s0) continue;
+        const ST* s = W.s + (long long)(grp + h) * W.N + col0;  // (grp: the first half's)
+        for (int c = lane; c < kCols; c += 32)
+            if (col0 + c < W.N) d[h * kCols + c] = s[c];
+    }
+}
+
+// First row of slice r of 2^lg: whole blocks, as even as they come.
+__host__ __device__ __forceinline__ int slice_row(int K, int r, int lg) {
+    const int blocks = (K + kBlock - 1) / kBlock;  // K <= 2^30: blocks * 8 fits
+    const int k = ((blocks * r) >> lg) * kBlock;
+    return k < K ? k : K;
+}
+
+// This warp's sums over part `part` of PARTS of the slice [k0, k1) of K, for
+// the 128 columns from col0 on and nt tokens, left in red [warp][token][128]
+// (over the rings: all warps are through with theirs).  tokens(): the token
+// rows, asked for once the first weight loads are on their way.  ring: this
+// warp's, 1024-byte aligned; bar: its barriers, initialised.  False: a copy
+// did not come (the sums are NaN).
+template <int NT8, int PARTS, typename XT, typename ST, bool TMA, typename F>
+__device__ __forceinline__ bool warp_sums(uint8_t* ring, uint64_t* bar, float* red, const Weight<ST>& W, int col0, int nt,
+                                          int k0, int k1, int part, F&& tokens) {
     using Cf = Cfg<NT8, ST>;
     constexpr bool BF = !std::is_same<XT, __half>::value;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
-    uint8_t* ring = smem + warp * Cf::RING;
     const int nblk = (k1 - k0 + kBlock - 1) / kBlock;
-    const int r0 = k0 + nblk * warp / kWarps * kBlock;
-    const int r1 = min(k1, k0 + nblk * (warp + 1) / kWarps * kBlock);
-    Loader<ST, VEC> ld;
-    ld.start(W, C, r0, lane);
-    const int blocks = nblk * (warp + 1) / kWarps - nblk * warp / kWarps;
-    const uint32_t ring0 = op::smem_u32(ring);
+    const int b0 = nblk * part / PARTS, blocks = nblk * (part + 1) / PARTS - b0;
+    const int r0 = k0 + b0 * kBlock, r1 = min(k1, r0 + blocks * kBlock);
+    const int stages = (blocks + 1) >> 1;
+    const uint32_t ring0 = op::smem_u32(ring), bar0 = op::smem_u32(bar);
+
+    // ---- loads: the next stage's row, its group and the rows until the group's end
+    int lrow = r0, grp = r0 / W.group, lleft = 0, lnext = W.group - (r0 - grp * W.group);
+    --grp;
+    auto scales_due = [&](bool& s0, bool& s1) {  // which halves of the stage begin a group (the warp's first does)
+        s0 = lleft == 0;
+        if (s0) lleft = lnext, lnext = W.group, ++grp;
+        lleft -= kBlock;
+        s1 = lleft == 0;
+        if (s1) lleft = W.group, ++grp;
+        lleft -= kBlock;
+    };
+    int xrow = 0;  // this lane's token's row (lanes below nt)
+    Tokens<XT> X{};
+    auto issue_w = [&](int s, uint32_t at) {  // the weight's and the scales' part of stage s
+        bool s0, s1;
+        scales_due(s0, s1);
+        if constexpr (TMA) {
+            if (lane == 0) {
+                const uint32_t b = bar0 + s * 8;
+                op::mbar_expect(b, kRows * 64 + nt * kXRow + ((s0 ? 1 : 0) + (s1 ? 1 : 0)) * kCols * (int)sizeof(ST));
+                op::tma_2d(at, W.qm, b, col0 >> 1, lrow);
+                if (s0) op::tma_2d(at + Cf::SOFF, W.sm, b, col0, grp - (s1 ? 1 : 0));
+                if (s1) op::tma_2d(at + Cf::SOFF + kCols * (int)sizeof(ST), W.sm, b, col0, grp);
+            }
+        } else {
+            load_plain<NT8, XT, ST>(ring + (at - ring0), W, col0, X, nt, lrow, r1, s0, s1, grp - (s1 ? 1 : 0), lane);
+        }
+    };
+    auto issue_x = [&](int s, uint32_t at) {
+        if constexpr (TMA) {
+            if (lane < nt) op::tma_2d(at + Cf::XOFF + lane * kXRow, X.map, bar0 + s * 8, lrow, xrow);
+        }
+        lrow += kRows;
+    };
+    const int pre = min(stages, Cf::STAGES);
+    if constexpr (!TMA) X = tokens();
 #pragma unroll
-    for (int i = 0; i < Cf::STAGES - 1; ++i)
-        if (i < blocks) ld.issue(ring0 + i * Cf::STAGE, ring + i * Cf::STAGE, C, lane);
-    const Tokens<XT> X = tokens();
-    XLoader<NT8, XT> xl;
-    xl.start(X, nt, r0, r1, lane);
+    for (int s = 0; s < Cf::STAGES; ++s)
+        if (s < pre) {
+            issue_w(s, ring0 + s * Cf::STAGE);
+            lrow += kRows;
+        }
+    lrow = r0;
+    if constexpr (TMA) {
+        X = tokens();
+        if (lane < nt) xrow = X.at(lane);
+    }
 #pragma unroll
-    for (int i = 0; i < Cf::STAGES - 1; ++i)
-        if (i < blocks) xl.issue(ring0 + i * Cf::STAGE + Cf::XOFF, ring + i * Cf::STAGE + Cf::XOFF, nt, lane);
-    // the first stages are one group; empty groups keep the count of the later ones
-#pragma unroll
-    for (int i = 0; i < Cf::STAGES - 1; ++i) op::cp_commit();
+    for (int s = 0; s < Cf::STAGES; ++s)
+        if (s < pre) issue_x(s, ring0 + s * Cf::STAGE);
+
     float factors = 1.f, f[NT8];
     if constexpr (BF) {
         if (blocks > 0) factors = find_factors(X, nt, r0, r1, lane);
@@ -453,49 +413,59 @@ __device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, c
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[n][i][c] = 0.f;
     }
-    // a matrix load's addresses: row l % 8 of row group l / 8 of the weight; token l % 8, rows 8 (l / 8) on
-    const uint32_t rows0 = ring0 + chunk_at(lane, 0), x0 = ring0 + Cf::XOFF + chunk_at(lane & 7, lane >> 3);
-    const uint32_t sc0 = ring0 + Cf::WORDS + 4 * g * (int)sizeof(ST);
+    // a matrix load's addresses: row l % 8 of row group l / 8 of the weight; token l % 8, values 8 (l / 8) on
+    const uint32_t rows0 = ring0 + chunk_at(lane, 0), x0 = ring0 + Cf::XOFF + token_at(lane & 7, lane >> 3);
+    const uint32_t sc0 = ring0 + Cf::SOFF + 4 * g * (int)sizeof(ST);
     float sc[16];
     int left = 0, next = W.group - r0 % W.group;  // rows that the scales at hand still cover; of the next ones
-    for (int i0 = 0; i0 < blocks; i0 += Cf::STAGES) {
+    bool ok = true;
+    uint32_t parity = 0;
+    int todo = stages - pre;  // stages still to load
+    for (int i0 = 0; i0 < stages && ok; i0 += Cf::STAGES, parity ^= 1u) {
 #pragma unroll
-        for (int j = 0; j < Cf::STAGES; ++j) {
-            if (i0 + j >= blocks) break;
-            op::cp_wait<Cf::STAGES - 2>();
-            __syncwarp();  // the copies are other lanes'
-            if (left == 0) {  // a group's first block brings its scales
-                if (i0 + j > 0) bias_fma<NT8>(acc, sc, b8);
+        for (int s = 0; s < Cf::STAGES; ++s) {
+            if (i0 + s >= stages) break;
+            if constexpr (TMA) {
+                ok = __all_sync(0xffffffffu, op::mbar_wait(bar0 + s * 8, parity));
+                if (!ok) break;
+            } else {
+                __syncwarp();
+            }
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    ST v[4];
-                    op::lds<4 * (int)sizeof(ST)>(v, sc0 + j * Cf::STAGE + 32 * h * (int)sizeof(ST));
+            for (int h = 0; h < 2; ++h) {
+                if (2 * (i0 + s) + h >= blocks) break;
+                if (left == 0) {  // a group's first rows bring its scales
+                    if (i0 + s + h > 0) bias_fma<NT8>(acc, sc, b8);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) sc[4 * h + c] = to_f32(v[c]);
+                    for (int q = 0; q < 4; ++q) {
+                        ST v[4];
+                        op::lds<4 * (int)sizeof(ST)>(v, sc0 + s * Cf::STAGE + (h * kCols + 32 * q) * (int)sizeof(ST));
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) sc[4 * q + c] = to_f32(v[c]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT8; ++n) b8[n][0] = b8[n][1] = b8[n][2] = b8[n][3] = 0.f;
+                    left = next;
+                    next = W.group;
                 }
-#pragma unroll
-                for (int n = 0; n < NT8; ++n) b8[n][0] = b8[n][1] = b8[n][2] = b8[n][3] = 0.f;
-                left = next;
-                next = W.group;
+                left -= kBlock;
+                block_fma<NT8, BF>(acc, b8, rows0 + s * Cf::STAGE + h * kBlock * 64,
+                                   (x0 + s * Cf::STAGE) ^ (h * 64), sc, f);
             }
-            left -= kBlock;
-            // (these copies go to the stage read one turn ago: every lane has
-            // passed this turn's __syncwarp since)
-            constexpr int LAST = Cf::STAGES - 1;
-            const int to = (j + LAST) % Cf::STAGES * Cf::STAGE;
-            if (i0 + j + LAST < blocks) {
-                ld.issue(ring0 + to, ring + to, C, lane);
-                xl.issue(ring0 + to + Cf::XOFF, ring + to + Cf::XOFF, nt, lane);
+            if (todo > 0) {
+                --todo;
+                __syncwarp();  // every lane has read the stage
+                issue_w(s, ring0 + s * Cf::STAGE);
+                issue_x(s, ring0 + s * Cf::STAGE);
             }
-            op::cp_commit();
-            block_fma<NT8, BF>(acc, b8, rows0 + j * Cf::STAGE, x0 + j * Cf::STAGE, sc, f);
         }
     }
     if (blocks > 0) bias_fma<NT8>(acc, sc, b8);
-    op::cp_wait<0>();
+    if (TMA && !ok) {  // let what is on its way arrive before the memory is used again
+        for (int s = 0; s < Cf::STAGES; ++s) op::mbar_wait(bar0 + s * 8, parity);
+    }
+    const float bad = ok ? 0.f : __int_as_float(0x7fffffff);
     __syncthreads();
-    // the quarters' sums, in their order
-    float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int n = 0; n < NT8; ++n)
 #pragma unroll
@@ -506,15 +476,26 @@ __device__ __forceinline__ void slice_sums(uint8_t* smem, const Weight<ST>& W, c
             if (tok < nt) {
                 float* o = red + (warp * NT8 * 8 + tok) * kCols + (c & 2);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[tile_col(i, g)] = acc[n][i][c] * ((i & 1) ? 0x1p20f : 0x1p24f) * inv;
+                for (int i = 0; i < 8; ++i)
+                    o[tile_col(i, g)] = acc[n][i][c] * ((i & 1) ? 0x1p20f : 0x1p24f) * inv + bad;
             }
         }
     __syncthreads();
+    return ok;
+}
+
+// Sum of element i (of [token][128]) over the PARTS warps from `first` on and
+// the cluster's slices, in their order: own(i) leaves the CTA's sum in place,
+// total(i) is read after the cluster's barrier.
+template <int NT8, int PARTS>
+__device__ __forceinline__ void join_parts(float* red, int first, int nt) {
+    constexpr int STRIDE = NT8 * 8 * kCols;
+    float* r = red + first * STRIDE;
     for (int i = threadIdx.x; i < nt * kCols; i += kThreads) {
-        float v = red[i];
+        float v = r[i];
 #pragma unroll
-        for (int q = 1; q < kWarps; ++q) v += red[q * NT8 * 8 * kCols + i];
-        red[i] = v;  // read and written by this thread alone
+        for (int q = 1; q < PARTS; ++q) v += r[q * STRIDE + i];
+        r[i] = v;  // read and written by this thread alone
     }
 }
 
@@ -527,43 +508,55 @@ __device__ __forceinline__ float cluster_total(const float* red, int i, int slic
     return v;
 }
 
-// First row of slice r of 2^lg: whole blocks, as even as they come.
-__host__ __device__ __forceinline__ int slice_row(int K, int r, int lg) {
-    const int blocks = (K + kBlock - 1) / kBlock;  // K <= 2^30: blocks * 8 fits
-    const int k = ((blocks * r) >> lg) * kBlock;
-    return k < K ? k : K;
+// This warp's ring and barriers in a kernel's shared memory; all threads.
+template <int NT8, typename ST>
+__device__ __forceinline__ uint8_t* rings(uint8_t* smem, uint64_t (&bar)[kWarps][3]) {
+    using Cf = Cfg<NT8, ST>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) {
+        for (int s = 0; s < Cf::STAGES; ++s) op::mbar_init(op::smem_u32(&bar[warp][s]), 1);
+        op::fence_mbar_init();
+    }
+    __syncwarp();
+    return smem + ((1024u - (op::smem_u32(smem) & 1023u)) & 1023u);
 }
 
 // Slices of K (a power of two) for a launch of `tiles` tiles: as many CTAs as
-// the SMs hold at once (per_sm each), a block at least for each warp, at most
+// the SMs hold at once (per_sm each), two at least for each warp (a stage), at most
 // a portable cluster.
 __host__ __forceinline__ int slices(long long tiles, int K, int sms, int per_sm) {
     const int blocks = (K + kBlock - 1) / kBlock;
     int S = 1;
-    while (S < 8 && 2 * tiles * S <= (long long)per_sm * sms && blocks >= 2 * S * kWarps) S *= 2;
+    while (S < 8 && 2 * tiles * S <= (long long)per_sm * sms && blocks >= 4 * S * kWarps) S *= 2;
     return S;
 }
 
 // ------------------------------------------------------------ the operator
 // y [T, N] = x [T, K] W.  Grid: (column tiles, token tiles, slices), the
 // slices of a tile one cluster.
-template <int NT8, typename XT, typename ST, bool VEC>
-__global__ void __launch_bounds__(kThreads, Cfg<NT8, ST>::PER_SM) int4_matvec_kernel(const XT* __restrict__ x, int T, Weight<ST> W,
-                                                               XT* __restrict__ y) {
+template <int NT8, typename XT, typename ST, bool TMA>
+__global__ void __launch_bounds__(kThreads, Cfg<NT8, ST>::PER_SM) int4_matvec_kernel(
+    const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap sm,
+    const __grid_constant__ CUtensorMap xm, const XT* __restrict__ x, int T, Weight<ST> W, XT* __restrict__ y) {
+    extern __shared__ __align__(16) uint8_t mv_smem[];
+    __shared__ uint64_t bar[kWarps][3];
+    uint8_t* base = rings<NT8, ST>(mv_smem, bar);
     op::pdl_enter();
-    extern __shared__ __align__(128) uint8_t mv_smem[];
+    const int warp = threadIdx.x >> 5;
     const int S = gridDim.z, slice = blockIdx.z, lg = __ffs(S) - 1;
     const int col0 = blockIdx.x * kCols;
     const int t0 = blockIdx.y * NT8 * 8, nt = min(NT8 * 8, T - t0);
-    const int k0 = slice_row(W.K, slice, lg), k1 = slice_row(W.K, slice + 1, lg);
-    const Columns C{col0, col0 + kHalf, W.N, W.N};
-    slice_sums<NT8, XT, ST, VEC>(mv_smem, W, C, nt, k0, k1, [&] { return Tokens<XT>{x, W.K, t0, nullptr, 1}; });
-    float* red = reinterpret_cast<float*>(mv_smem);
+    W.qm = &qm;
+    W.sm = &sm;
+    float* red = reinterpret_cast<float*>(base);
+    warp_sums<NT8, kWarps, XT, ST, TMA>(base + warp * Cfg<NT8, ST>::RING, bar[warp], red, W, col0, nt,
+                                        slice_row(W.K, slice, lg), slice_row(W.K, slice + 1, lg), warp,
+                                        [&] { return Tokens<XT>{&xm, x, W.K, t0, nullptr, 1}; });
+    join_parts<NT8, kWarps>(red, 0, nt);
     if (S > 1) op::cluster_sync();
     else __syncthreads();
-    const int items = nt * kCols;
-    const int i0 = (items >> lg) * slice, i1 = i0 + (items >> lg);  // items is a multiple of 8
-    for (int i = i0 + threadIdx.x; i < i1; i += kThreads) {
+    const int items = nt * kCols >> lg;  // nt * 128 is a multiple of 8
+    for (int i = items * slice + threadIdx.x; i < items * (slice + 1); i += kThreads) {
         const int tok = i / kCols, n = col0 + i % kCols;
         if (n >= W.N) continue;
         const float v = cluster_total(red, i, S);
@@ -575,16 +568,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT8, ST>::PER_SM) int4_matvec_ke
 }
 
 // ----------------------------------------------------------- the layer's experts
-// The codes and scales of every expert and of the shared one (index E), by
-// value: the launch carries them, so there is no table to upload or to keep.
-struct Experts {
-    const uint8_t* q[kMaxGroups];
-    const void* s[kMaxGroups];
-};
-
-// A launch's rows and outputs for its routed experts and the shared one.
+// A launch's experts, rows and outputs, for its routed experts [0] and the
+// shared one [1].
 struct Rows {
-    const void* x[2];        // operand rows: routed (slot order, or x itself: gather), shared (token order)
+    CUtensorMap xm[2];       // operand rows: routed (slot order, or by gather), shared (token order)
+    const CUtensorMap* qm;   // codes of experts 0 .. E - 1 and of the shared one (E), then
+    const CUtensorMap* sm;   // their scales
     int K[2], N[2];          // the weights' rows and columns
     const float* scale[2];   // gate/up: what multiplies a row's sums (null: 1)
     __half* h[2];            // gate/up: hidden rows [., N / 2]
@@ -592,101 +581,101 @@ struct Rows {
     const int32_t* perm;
     int k;
     bool gather;             // routed operand row = x[perm[slot] / k]
-    int shared_rows;         // > 0: the shared expert's rows, its units the first ones (it is not in the list)
+    int shared_rows;         // > 0: the shared expert's rows; its units are the first ones and not in the list
+    const int4* units;       // the other units as (expert, first slot, rows, -), rows = 0 past the last; null: by tab
+    const GroupTable* tab;
+    int num_experts, group;
     unsigned* err;
 };
 
-// Which group and rows unit u of the work list is: units are the groups'
-// tiles of 8 rows, in the list's order.  All threads; false past the list.
-__device__ __forceinline__ bool find_unit(const GroupTable* tab, int u, int& group, int& row) {
-    __shared__ int s_group, s_row;
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x, n = tab->num_groups;
-        int base = 0, found = -1, at = 0;
-        for (int g0 = 0; g0 < n && found < 0; g0 += 32) {
-            const int tiles = g0 + lane < n ? (tab->rows[g0 + lane] + 7) >> 3 : 0;
-            int incl = tiles;
+// The group and first row of unit u of a work list: units are the groups'
+// tiles of 8 rows, in the list's order.  One warp; group < 0 past the list.
+__device__ __forceinline__ int2 find_unit(const GroupTable* tab, int u) {
+    const int lane = threadIdx.x & 31, n = tab->num_groups;
+    int base = 0;
+    for (int g0 = 0; g0 < n; g0 += 32) {
+        const int tiles = g0 + lane < n ? (tab->rows[g0 + lane] + 7) >> 3 : 0;
+        int incl = tiles;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            const bool here = u < base + incl && u >= base + incl - tiles;
-            const unsigned who = __ballot_sync(0xffffffffu, here);
-            if (who) {
-                const int l = __ffs(who) - 1;
-                found = g0 + l;
-                at = u - base - __shfl_sync(0xffffffffu, incl - tiles, l);
-            }
-            base += __shfl_sync(0xffffffffu, incl, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
         }
-        if (lane == 0) {
-            s_group = found;
-            s_row = at * 8;
+        const unsigned who = __ballot_sync(0xffffffffu, u < base + incl);
+        if (who) {
+            const int l = __ffs(who) - 1;
+            return make_int2(g0 + l, (u - base - __shfl_sync(0xffffffffu, incl - tiles, l)) * 8);
         }
+        base += __shfl_sync(0xffffffffu, incl, 31);
     }
-    __syncthreads();
-    group = s_group;
-    row = s_row;
-    return group >= 0;
+    return make_int2(-1, 0);
 }
 
 // Gate/up: h = silu(c a_gate) (c a_up), c the row's scale (its sigmoid gate).
 // Down: the fp32 sums, un-permuted.  Grid: (column tiles, units, slices); a
-// gate/up tile is 64 hidden columns (gate in the first half, up in the
-// second), a down tile 128 columns.
-template <typename XT, typename ST, bool GATE_UP>
-__global__ void __launch_bounds__(kThreads, Cfg<1, ST>::PER_SM) experts_kernel(const GroupTable* tab, int num_experts,
-                                                                              int group_rows,
-                                                                              const __grid_constant__ Experts E,
-                                                                              const Rows R) {
-    extern __shared__ __align__(128) uint8_t mv_smem[];
-    // the shared expert's units come first and read nothing that the routing
-    // before this launch writes: they need not wait for it
+// tile is 128 hidden columns (gate/up) or 128 columns (down).
+template <typename ST, bool GATE_UP>
+__global__ void __launch_bounds__(kThreads, Cfg<1, ST>::PER_SM) experts_kernel(const __grid_constant__ Rows R) {
+    extern __shared__ __align__(16) uint8_t mv_smem[];
+    __shared__ uint64_t bar[kWarps][3];
+    uint8_t* base = rings<1, ST>(mv_smem, bar);
+    const int warp = threadIdx.x >> 5;
+    // the shared expert's units come first: their weights are on their way
+    // before what the launch before this one writes is waited for
     const int shared_units = (R.shared_rows + 7) >> 3;
-    const bool early = GATE_UP && (int)blockIdx.y < shared_units;
-    if (!early) op::pdl_wait();
+    const bool first = (int)blockIdx.y < shared_units;
+    if (!first) op::pdl_wait();
     op::pdl_launch();
     int expert, sh, nt, row0;
-    if ((int)blockIdx.y < shared_units) {
-        expert = num_experts, sh = 1;
+    if (first) {
+        expert = R.num_experts, sh = 1;
         row0 = blockIdx.y * 8;
         nt = min(8, R.shared_rows - row0);
+    } else if (R.units) {
+        const int4 u = __ldg(R.units + (blockIdx.y - shared_units));
+        expert = u.x, row0 = u.y, nt = u.z, sh = 0;
+        if (nt == 0) return;
     } else {
-        int grp, row;
-        if (!find_unit(tab, blockIdx.y - shared_units, grp, row)) return;
-        expert = tab->expert[grp], sh = expert == num_experts ? 1 : 0;
-        nt = min(8, tab->rows[grp] - row), row0 = tab->row0[grp] + row;
+        const int2 at = find_unit(R.tab, blockIdx.y);
+        if (at.x < 0) return;
+        expert = R.tab->expert[at.x], sh = expert == R.num_experts ? 1 : 0;
+        nt = min(8, R.tab->rows[at.x] - at.y), row0 = R.tab->row0[at.x] + at.y;
     }
-    const int K = R.K[sh], N = R.N[sh];
-    const int F = N / 2;
-    const int col0 = blockIdx.x * (GATE_UP ? kHalf : kCols);
-    if (col0 >= (GATE_UP ? F : N)) return;
+    const int K = R.K[sh], N = R.N[sh], width = GATE_UP ? N / 2 : N;
+    const int c0 = blockIdx.x * kCols;
+    if (c0 >= width) {
+        if (first) op::pdl_wait();
+        return;
+    }
     const int S = gridDim.z, slice = blockIdx.z, lg = __ffs(S) - 1;
     const int k0 = slice_row(K, slice, lg), k1 = slice_row(K, slice + 1, lg);
-    const Weight<ST> W{E.q[expert], static_cast<const ST*>(E.s[expert]), N / 2, N, K, group_rows};
-    const Columns C{col0, GATE_UP ? F + col0 : col0 + kHalf, GATE_UP ? F : N, N};
-    slice_sums<1, XT, ST, true>(mv_smem, W, C, nt, k0, k1, [&] {
-        return Tokens<XT>{static_cast<const XT*>(R.x[sh]), K, row0, GATE_UP && R.gather && !sh ? R.perm : nullptr, R.k};
-    });
-    const float* red = reinterpret_cast<const float*>(mv_smem);
+    const Weight<ST> W{R.qm + expert, R.sm + expert, nullptr, nullptr, N, K, R.group};
+    constexpr int PARTS = GATE_UP ? kWarps / 2 : kWarps;
+    const int side = warp / PARTS;  // gate/up: 0 gate, 1 up
+    float* red = reinterpret_cast<float*>(base);
+    const bool ok = warp_sums<1, PARTS, __half, ST, true>(
+        base + warp * Cfg<1, ST>::RING, bar[warp], red, W, side * width + c0, nt, k0, k1, warp - side * PARTS, [&] {
+            if (first) op::pdl_wait();
+            return Tokens<__half>{&R.xm[sh], nullptr, K, row0, GATE_UP && R.gather && !sh ? R.perm : nullptr, R.k};
+        });
+    if (!ok && (threadIdx.x & 31) == 0) atomicOr(R.err, kErrTimeout);
+    join_parts<1, PARTS>(red, 0, nt);
+    if (GATE_UP) join_parts<1, PARTS>(red, PARTS, nt);
     if (S > 1) op::cluster_sync();
     else __syncthreads();
-    const int width = GATE_UP ? kHalf : kCols, items = nt * width;
-    const int i0 = (items >> lg) * slice, i1 = i0 + (items >> lg);  // items is a multiple of 8
-    for (int i = i0 + threadIdx.x; i < i1; i += kThreads) {
-        const int tok = i / width, c = i % width;
+    const int items = nt * kCols >> lg;  // nt * 128 is a multiple of 8
+    for (int i = items * slice + threadIdx.x; i < items * (slice + 1); i += kThreads) {
+        const int tok = i / kCols, c = c0 + i % kCols, row = row0 + tok;
+        if (c >= width) continue;
         if (GATE_UP) {
-            if (col0 + c >= F) continue;
-            const float g = R.scale[sh] ? R.scale[sh][row0 + tok] : 1.0f;
-            const float a = g * cluster_total(red, tok * kCols + c, S), b = g * cluster_total(red, tok * kCols + kHalf + c, S);
+            const float g = R.scale[sh] ? R.scale[sh][row] : 1.0f;
+            const float a = g * cluster_total(red, i, S), b = g * cluster_total(red, PARTS * 8 * kCols + i, S);
             const float hv = __fdividef(a, 1.0f + __expf(-a)) * b;
             if (!(fabsf(hv) < 65520.0f)) atomicOr(R.err, kErrF16Range);  // rounds to infinity in f16
-            R.h[sh][(long long)(row0 + tok) * F + col0 + c] = __float2half_rn(hv);
+            R.h[sh][(long long)row * width + c] = __float2half_rn(hv);
         } else {
-            if (col0 + c >= N) continue;
-            const int orow = sh ? row0 + tok : R.perm[row0 + tok];
-            R.part[sh][(long long)orow * N + col0 + c] = cluster_total(red, i, S);
+            const int orow = sh ? row : R.perm[row];
+            R.part[sh][(long long)orow * width + c] = cluster_total(red, i, S);
         }
     }
     if (S > 1) op::cluster_sync();

@@ -31,44 +31,11 @@
 #include "route_group.cuh"
 #include "route_small.cuh"
 #include "router.cuh"
+#include "tensor_map.cuh"
 
 using namespace l4moe;
 
 namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
-// 2-D row-major tensor [outer, inner] with 128-byte swizzled boxes.
-bool encode_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner,
-               uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
-               CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return false;
-    cuuint64_t dims[2] = {inner, outer};
-    cuuint64_t strides[1] = {row_bytes};
-    cuuint32_t box[2] = {box_inner, box_outer};
-    cuuint32_t estr[2] = {1, 1};
-    return enc(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 // Split-K is used for batches of at most this many tokens, into at most
 // kMaxSplit k-ranges (tiles too few to fill the GPU, e.g. decode).
@@ -248,8 +215,9 @@ struct l4moe_handle {
     std::vector<const void*> key_gu, key_dn;
     const void* key_sgu = nullptr;
     const void* key_sdn = nullptr;
-    std::vector<CUtensorMap> h_maps;  // [2][E+1]: gate/up set then down set; capacity
-                                      // reserved at creation, so its address is fixed
+    std::vector<CUtensorMap> h_maps;  // [2][E+1]: gate/up set then down set (group scales: [4][E+1],
+                                      // with the scales' maps after each set); capacity reserved at
+                                      // creation, so its address is fixed
     std::vector<const void*> hkey_gu, hkey_dn;  // weights h_maps was encoded for
     const void* hkey_sgu = nullptr;
     const void* hkey_sdn = nullptr;
@@ -334,6 +302,38 @@ l4moe_status ensure_workspace(l4moe_handle* h, int T) {
     return L4MOE_OK;
 }
 
+// Descriptors of a layer's weights: codes or values, and with group scales
+// the scales' too.
+size_t weight_map_count(const l4moe_handle* h) { return (h->group ? 4 : 2) * (size_t)(h->p.num_experts + 1); }
+
+// Group scales: maps of the products' boxes (64 rows by 128 columns of codes,
+// one row by 128 columns of scales), [gate/up codes][gate/up scales][down
+// codes][down scales] of the experts and the shared one.
+bool encode_group_maps(l4moe_handle* h, const void* const* Wgu, const void* const* Wdn, const void* Wsgu,
+                       const void* Wsdn) {
+    const int E = h->p.num_experts, n = E + 1, G = h->group;
+    const uint64_t es = h->group_type == L4MOE_ELEM_F32 ? 4 : 2;
+    const CUtensorMapDataType st = h->group_type == L4MOE_ELEM_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : h->group_type == L4MOE_ELEM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    h->h_maps.assign(4 * n, CUtensorMap{});
+    for (int e = 0; e <= E; ++e) {
+        const uint64_t f = e == E ? h->p.shared_ffn : h->p.expert_ffn, d = h->p.d_model;
+        const void* q[2] = {e == E ? Wsgu : Wgu[e], e == E ? Wsdn : Wdn[e]};
+        const uint64_t K[2] = {d, f}, N[2] = {2 * f, d};
+        for (int i = 0; i < 2; ++i) {
+            if (!encode_2d(&h->h_maps[2 * i * n + e], CU_TENSOR_MAP_DATA_TYPE_UINT8, q[i], N[i] / 2, K[i], N[i] / 2, 64,
+                           mv::kRows, CU_TENSOR_MAP_SWIZZLE_64B) ||
+                !encode_2d(&h->h_maps[(2 * i + 1) * n + e], st, h->scale_tab[i * n + e], N[i], (K[i] + G - 1) / G,
+                           N[i] * es, mv::kCols, 1, CU_TENSOR_MAP_SWIZZLE_NONE)) {
+                h->h_maps.clear();
+                return false;
+            }
+        }
+    }
+    return true;
+}
+
 // Encode the weight descriptors on the host (h->h_maps) unless they already
 // describe these pointers.
 l4moe_status encode_weight_maps(l4moe_handle* h, const void* const* Wgu, const void* const* Wdn,
@@ -343,6 +343,18 @@ l4moe_status encode_weight_maps(l4moe_handle* h, const void* const* Wgu, const v
     for (int e = 0; same && e < E; ++e) same = h->hkey_gu[e] == Wgu[e] && h->hkey_dn[e] == Wdn[e];
     if (same) return L4MOE_OK;
     const int d = h->p.d_model, F = h->p.expert_ffn, Fs = h->p.shared_ffn;
+    if (h->group) {
+        h->hkey_gu.clear();
+        if (!encode_group_maps(h, Wgu, Wdn, Wsgu, Wsdn))
+            return fail(h, L4MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for a weight with group scales");
+        if (E > 0) {
+            h->hkey_gu.assign(Wgu, Wgu + E);
+            h->hkey_dn.assign(Wdn, Wdn + E);
+        }
+        h->hkey_sgu = Wsgu;
+        h->hkey_sdn = Wsdn;
+        return L4MOE_OK;
+    }
     const l4moe_dtype wdt = h->p.dtype;
     CUtensorMapDataType dt = wdt == L4MOE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                              : wdt == L4MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -385,6 +397,13 @@ l4moe_status encode_weight_maps(l4moe_handle* h, const void* const* Wgu, const v
     return L4MOE_OK;
 }
 
+// Encode the weight descriptors again at the next forward.
+void forget_weight_maps(l4moe_handle* h) {
+    h->h_maps.clear();
+    h->hkey_sgu = h->hkey_sdn = nullptr;
+    h->key_sgu = h->key_sdn = nullptr;
+}
+
 // (Re)build and upload the weight descriptors when any weight pointer changed.
 l4moe_status ensure_weight_maps(l4moe_handle* h, const void* const* Wgu, const void* const* Wdn,
                                 const void* Wsgu, const void* Wsdn, cudaStream_t st) {
@@ -395,11 +414,13 @@ l4moe_status ensure_weight_maps(l4moe_handle* h, const void* const* Wgu, const v
     l4moe_status s = encode_weight_maps(h, Wgu, Wdn, Wsgu, Wsdn);
     if (s != L4MOE_OK) return s;
     if (!h->d_maps) {
-        cudaError_t e = cudaMalloc(&h->d_maps, sizeof(CUtensorMap) * 2 * (E + 1));
+        // (room for the scales' descriptors too, so that a change of the kind of scales keeps the array)
+        const size_t cap = (h->p.dtype == L4MOE_INT4 ? 4 : 2) * (size_t)(E + 1);
+        cudaError_t e = cudaMalloc(&h->d_maps, sizeof(CUtensorMap) * cap);
         if (e != cudaSuccess) return cuda_fail(h, e, "descriptor cudaMalloc");
     }
     // pageable source: returns once the bytes are staged, so h_maps may change later
-    cudaError_t e = cudaMemcpyAsync(h->d_maps, h->h_maps.data(), sizeof(CUtensorMap) * 2 * (E + 1),
+    cudaError_t e = cudaMemcpyAsync(h->d_maps, h->h_maps.data(), sizeof(CUtensorMap) * weight_map_count(h),
                                     cudaMemcpyHostToDevice, st);
     if (e != cudaSuccess) return cuda_fail(h, e, "descriptor upload");
     h->key_gu.assign(Wgu, Wgu + E);
@@ -460,31 +481,22 @@ void launch_gemm(int grid, const BMaps& bm, const GemmArgs& a, cudaStream_t st, 
     launch_gemm_pair<MODE, ET, WQ>(grid, bm, a, bm, a, st, small);
 }
 
-// The weights of one forward whose experts have group scales: the pointers
-// themselves (the launches carry them).
-struct ExpertWeights {
-    const void* const* gate_up;
-    const void* const* down;
-    const void *shared_gate_up, *shared_down;
-};
-
-template <typename XT, typename ST, bool GATE_UP>
-void launch_experts_t(dim3 grid, cudaStream_t st, const GroupTable* tab, int E, int group, const mv::Experts& ptrs,
-                      const mv::Rows& rows) {
+// Experts with group scales: `units` units at most of `tiles` column tiles, K
+// split into `slices`.
+template <typename ST, bool GATE_UP>
+void launch_experts_t(dim3 grid, cudaStream_t st, const mv::Rows& rows) {
     constexpr size_t smem = mv::Cfg<1, ST>::SMEM;
     static std::atomic<uint64_t> attr_done{0};
-    ensure_smem_attr(attr_done, mv::experts_kernel<XT, ST, GATE_UP>, smem);
-    launch_kc(mv::experts_kernel<XT, ST, GATE_UP>, grid, dim3(mv::kThreads), smem, st, grid.z > 1 ? grid.z : 0u, tab,
-              E, group, ptrs, rows);
+    ensure_smem_attr(attr_done, mv::experts_kernel<ST, GATE_UP>, smem);
+    launch_kc(mv::experts_kernel<ST, GATE_UP>, grid, dim3(mv::kThreads), smem, st, grid.z > 1 ? grid.z : 0u, rows);
 }
 
-template <typename XT, bool GATE_UP>
-void launch_experts(l4moe_elem type, dim3 grid, cudaStream_t st, const GroupTable* tab, int E, int group,
-                    const mv::Experts& ptrs, const mv::Rows& rows) {
-    if (type == L4MOE_ELEM_F32) launch_experts_t<XT, float, GATE_UP>(grid, st, tab, E, group, ptrs, rows);
-    else if (type == L4MOE_ELEM_BF16)
-        launch_experts_t<XT, __nv_bfloat16, GATE_UP>(grid, st, tab, E, group, ptrs, rows);
-    else launch_experts_t<XT, __half, GATE_UP>(grid, st, tab, E, group, ptrs, rows);
+template <bool GATE_UP>
+void launch_experts(l4moe_elem type, int tiles, int units, int slices, cudaStream_t st, const mv::Rows& rows) {
+    const dim3 grid(tiles, units, slices);
+    if (type == L4MOE_ELEM_F32) launch_experts_t<float, GATE_UP>(grid, st, rows);
+    else if (type == L4MOE_ELEM_BF16) launch_experts_t<__nv_bfloat16, GATE_UP>(grid, st, rows);
+    else launch_experts_t<__half, GATE_UP>(grid, st, rows);
 }
 
 // The launch sequence of one forward.  w / ws_tokens: the workspace and the
@@ -497,11 +509,11 @@ void launch_experts(l4moe_elem type, dim3 grid, cudaStream_t st, const GroupTabl
 template <typename ET, int WQ = kWqNone>
 l4moe_status run_layer(l4moe_handle* h, int T, const void* x, const void* Wr, const void* Wsgu,
                        const void* Wsdn, void* out, cudaStream_t st, uint8_t* w, int ws_tokens,
-                       const CUtensorMap* maps, const float* const* scales = nullptr,
-                       const ExpertWeights* grouped = nullptr) {
+                       const CUtensorMap* maps, const float* const* scales = nullptr) {
     constexpr bool FP8W = WQ != kWqNone;  // coded weights with per-column scales
     constexpr bool ACT8 = WQ == kWqAct8;  // and E4M3 token rows (FP8 activation mode)
     const l4moe_params& p = h->p;
+    const bool grouped = WQ == kWqInt4 && h->group > 0;  // experts with group scales
     const int d = p.d_model, F = p.expert_ffn, Fs = p.shared_ffn, E = p.num_experts;
     const WsLayout L = ws_layout(p, ws_tokens, h->sms, h->top_k, h->act8);
     unsigned* err = reinterpret_cast<unsigned*>(w + L.err);
@@ -598,6 +610,8 @@ l4moe_status run_layer(l4moe_handle* h, int T, const void* x, const void* Wr, co
     // experts with group scales, a few tokens: routing without row copies
     // (the products gather their bf16 rows themselves)
     const bool gather = grouped && E > 0 && T <= rg::kTokens && E % 8 == 0;
+    // tiles of 8 rows of one expert: every one holds an entry
+    const int routed_units = E > 0 ? std::min(Tv, std::min(E, Tv) + Tv / 8) : 0;
     if (gather) {
         static std::atomic<uint64_t> attr_done{0};
         ensure_smem_attr(attr_done, rg::route_group_kernel, rg::smem_bytes());
@@ -605,7 +619,8 @@ l4moe_status run_layer(l4moe_handle* h, int T, const void* x, const void* Wr, co
         launch_cluster_x(rg::route_group_kernel, dim3(rg::kCtas), dim3(rg::kThreads), rg::smem_bytes(), st,
                          (unsigned)rg::kCtas, static_cast<const __nv_bfloat16*>(x),
                          static_cast<const __nv_bfloat16*>(Wr), (const float*)h->bias, T, d, E, k, idx, gate, lmax,
-                         margin, counts, offsets, perm, gslot, tab_gu);
+                         margin, counts, offsets, perm, gslot, reinterpret_cast<int4*>(tab_gu), routed_units,
+                         reinterpret_cast<__half*>(w + L.x16), tokscale);
         t_router.stop();
         L4MOE_CHECK_LAUNCH("grouped routing launch");
     } else if (E > 0 && T <= kSmallMaxTokens) {
@@ -731,50 +746,52 @@ l4moe_status run_layer(l4moe_handle* h, int T, const void* x, const void* Wr, co
             // 8 rows, the sums of a token added by the down finish
             const bool has = E > 0;
             mv::Rows R{};
-            R.x[0] = gather ? x : (const void*)xg;
-            R.x[1] = gather ? x : (const void*)x16;
+            // operand rows: boxes of one row by 64 values
+            auto rows_map = [&](CUtensorMap* m, const void* base, int width, int n) {
+                return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, (uint64_t)width, (uint64_t)n,
+                                 2 * (uint64_t)width, mv::kRows, 1);
+            };
+            const int units = routed_units + (T + 7) / 8, per_sm = mv::Cfg<1, float>::PER_SM;
+            if (units > 65535) return fail(h, L4MOE_ERR_ARG, "batch too long for experts with group scales");
+            // without experts the routed operand is never read
+            if (!rows_map(&R.xm[0], gather || !has ? x16 : xg, d, gather || !has ? T : Tv) ||
+                !rows_map(&R.xm[1], x16, d, T))
+                return fail(h, L4MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for an activation");
             R.gather = gather;
             R.perm = perm;
             R.k = k;
             R.shared_rows = gather ? T : 0;
+            R.units = gather ? reinterpret_cast<const int4*>(tab_gu) : nullptr;
+            R.tab = tab_gu;
+            R.num_experts = E;
+            R.group = h->group;
+            R.qm = maps;
+            R.sm = maps + (E + 1);
             R.K[0] = R.K[1] = d;
             R.N[0] = 2 * F, R.N[1] = 2 * Fs;
-            R.scale[0] = gslot, R.scale[1] = gather ? nullptr : tokscale;
+            R.scale[0] = gslot, R.scale[1] = tokscale;
             R.h[0] = hr, R.h[1] = hs;
             R.err = err;
-            mv::Experts ptrs;
-            auto fill = [&](const void* const* q, const void* qs, int first) {
-                for (int e = 0; e < E; ++e) {
-                    ptrs.q[e] = static_cast<const uint8_t*>(q[e]);
-                    ptrs.s[e] = h->scale_tab[first + e];
-                }
-                ptrs.q[E] = static_cast<const uint8_t*>(qs);
-                ptrs.s[E] = h->scale_tab[first + E];
-            };
-            // tiles of 8 rows: every routed one holds an entry
-            const int units = (has ? std::min(Tv, std::min(E, Tv) + Tv / 8) : 0) + (T + 7) / 8;
-            if (units > 65535) return fail(h, L4MOE_ERR_ARG, "batch too long for experts with group scales");
-            const int gt = (std::max(has ? F : 0, Fs) + mv::kHalf - 1) / mv::kHalf, dt = (d + mv::kCols - 1) / mv::kCols;
-            const int sg = mv::slices((long long)gt * units, d, h->sms, mv::Cfg<1, float>::PER_SM);
-            const int sd = mv::slices((long long)dt * units, has ? std::min(F, Fs) : Fs, h->sms, mv::Cfg<1, float>::PER_SM);
-            fill(grouped->gate_up, grouped->shared_gate_up, 0);
+            const int gt = (std::max(has ? F : 0, Fs) + mv::kCols - 1) / mv::kCols, dt = (d + mv::kCols - 1) / mv::kCols;
+            // (gate/up: a warp's part is half of a slice, so half the rows make do)
+            const int sg = mv::slices((long long)gt * units, 2 * d, h->sms, per_sm);
             {
                 LaunchTimer t_gu(h, 3, st);
-                const dim3 grid(gt, units, sg);
-                if (gather) launch_experts<__nv_bfloat16, true>(h->group_type, grid, st, tab_gu, E, h->group, ptrs, R);
-                else launch_experts<__half, true>(h->group_type, grid, st, tab_gu, E, h->group, ptrs, R);
+                launch_experts<true>(h->group_type, gt, units, sg, st, R);
                 t_gu.stop();
                 L4MOE_CHECK_LAUNCH("grouped gate/up launch");
             }
-            fill(grouped->down, grouped->shared_down, E + 1);
             float* part = reinterpret_cast<float*>(w + L.part);
-            R.x[0] = hr, R.x[1] = hs;
+            if (!rows_map(&R.xm[0], has ? hr : hs, has ? F : Fs, has ? Tv : T) || !rows_map(&R.xm[1], hs, Fs, T))
+                return fail(h, L4MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for an activation");
+            R.qm = maps + 2 * (E + 1);
+            R.sm = maps + 3 * (E + 1);
             R.K[0] = F, R.K[1] = Fs;
             R.N[0] = R.N[1] = d;
             R.part[0] = part, R.part[1] = part + (size_t)(has ? Tv : 0) * d;
+            const int sd = mv::slices((long long)dt * units, has ? std::min(F, Fs) : Fs, h->sms, per_sm);
             LaunchTimer t_dn(h, 4, st);
-            launch_experts<__half, false>(h->group_type, dim3(dt, units, sd), st, gather ? tab_gu : tab_dn, E,
-                                          h->group, ptrs, R);
+            launch_experts<false>(h->group_type, dt, units, sd, st, R);
             L4MOE_CHECK_LAUNCH("grouped down launch");
             const long long n = (long long)T * d;
             launch_k(down_finish_kernel<ET>, dim3((int)std::min<long long>((n / 4 + 255) / 256, 8LL * h->sms)),
@@ -986,12 +1003,9 @@ l4moe_status forward_impl(l4moe_handle* h, int T, const void* x, const void* Wr,
                           const void* Wsdn, void* out, cudaStream_t st) {
     l4moe_status s;
     if ((s = ensure_workspace(h, T)) != L4MOE_OK) return s;
-    if (h->group) {
-        const ExpertWeights g{Wgu, Wdn, Wsgu, Wsdn};
-        return run_layer<__nv_bfloat16, kWqInt4>(h, T, x, Wr, Wsgu, Wsdn, out, st, h->ws, h->ws_tokens, nullptr,
-                                                 nullptr, &g);
-    }
     if ((s = ensure_weight_maps(h, Wgu, Wdn, Wsgu, Wsdn, st)) != L4MOE_OK) return s;
+    if (h->group)
+        return run_layer<__nv_bfloat16, kWqInt4>(h, T, x, Wr, Wsgu, Wsdn, out, st, h->ws, h->ws_tokens, h->d_maps);
     if (coded8(h->p.dtype) && (s = ensure_scales(h, st)) != L4MOE_OK) return s;
     switch (h->p.dtype) {
     case L4MOE_F32:
@@ -1063,8 +1077,7 @@ l4moe_status l4moe_forward_static(l4moe_handle* h, int T, const void* x, const v
     const int E = h->p.num_experts;
     const bool fp8 = coded8(h->p.dtype);
     const size_t ws_bytes = (ws_layout(h->p, T, h->sms, h->top_k, h->act8).device_total + 255) & ~size_t(255);
-    // (experts with group scales: the launches carry the pointers)
-    const size_t maps_bytes = h->group ? 0 : sizeof(CUtensorMap) * 2 * (E + 1);
+    const size_t maps_bytes = sizeof(CUtensorMap) * weight_map_count(h);
     const size_t scales_bytes = fp8 && !h->group ? sizeof(float*) * 2 * (E + 1) : 0;
     if (ws_bytes + maps_bytes + scales_bytes > L4MOE_STATIC_WORKSPACE_BYTES) {
         char msg[200];
@@ -1079,12 +1092,9 @@ l4moe_status l4moe_forward_static(l4moe_handle* h, int T, const void* x, const v
     CUtensorMap* maps = reinterpret_cast<CUtensorMap*>(base + ws_bytes);
     // every call shares the array: upload this call's descriptors and clear
     // the state a forward expects to start at zero
-    cudaError_t e = cudaSuccess;
-    if (!h->group) {
-        if ((s = encode_weight_maps(h, W_gate_up, W_down, Ws_gate_up, Ws_down)) != L4MOE_OK) return s;
-        e = cudaMemcpyAsync(maps, h->h_maps.data(), maps_bytes, cudaMemcpyHostToDevice, st);
-        if (e != cudaSuccess) return cuda_fail(h, e, "static descriptor upload");
-    }
+    if ((s = encode_weight_maps(h, W_gate_up, W_down, Ws_gate_up, Ws_down)) != L4MOE_OK) return s;
+    cudaError_t e = cudaMemcpyAsync(maps, h->h_maps.data(), maps_bytes, cudaMemcpyHostToDevice, st);
+    if (e != cudaSuccess) return cuda_fail(h, e, "static descriptor upload");
     // the error word, the routing kernels' ticket and the fused GEMM's two
     // tile counters that follow it
     e = cudaMemsetAsync(base + ws_layout(h->p, T, h->sms, h->top_k, h->act8).err, 0, 4 * sizeof(unsigned), st);
@@ -1098,10 +1108,8 @@ l4moe_status l4moe_forward_static(l4moe_handle* h, int T, const void* x, const v
     }
     const unsigned timing = h->timing;  // event timing would create events: off here
     h->timing = 0;
-    const ExpertWeights grouped{W_gate_up, W_down, Ws_gate_up, Ws_down};
     if (h->group)
-        s = run_layer<__nv_bfloat16, kWqInt4>(h, T, x, W_router, Ws_gate_up, Ws_down, out, st, base, T, nullptr,
-                                              nullptr, &grouped);
+        s = run_layer<__nv_bfloat16, kWqInt4>(h, T, x, W_router, Ws_gate_up, Ws_down, out, st, base, T, maps);
     else if (h->p.dtype == L4MOE_F32)
         s = run_layer<float>(h, T, x, W_router, Ws_gate_up, Ws_down, out, st, base, T, maps);
     else if (h->p.dtype == L4MOE_FP8_E4M3 && h->act8)
@@ -1166,7 +1174,7 @@ l4moe_status l4moe_create(const l4moe_params* params, l4moe_handle** out) {
     h->p = p;
     h->device = dev;
     h->sms = sms;
-    h->h_maps.reserve(2 * (size_t)(p.num_experts + 1));
+    h->h_maps.reserve(4 * (size_t)(p.num_experts + 1));
     h->scale_tab.assign(2 * (size_t)(p.num_experts + 1), nullptr);
     *out = h;
     return L4MOE_OK;
@@ -1279,6 +1287,7 @@ l4moe_status l4moe_set_weight_scales(l4moe_handle* h, const float* const* s_gate
     h->ss_dn = ss_down;
     fill_scale_table(h);
     h->scales_dirty = true;
+    if (h->group) forget_weight_maps(h);
     h->group = 0;
     return L4MOE_OK;
 }
@@ -1310,6 +1319,7 @@ l4moe_status l4moe_set_group_scales(l4moe_handle* h, int group, l4moe_elem type,
     h->scales_dirty = true;
     h->group = group;
     h->group_type = type;
+    forget_weight_maps(h);  // they hold the scales' addresses
     return L4MOE_OK;
 }
 

@@ -9,12 +9,15 @@
 // tokens' rows as the other operand straight from global memory; the warps'
 // sums are added through shared memory, the CTAs' through distributed shared
 // memory by the CTA that then selects the token's experts, and the first CTA
-// makes the slots.  All sums in a fixed order.  No rows are copied.
+// makes the slots.  All sums in a fixed order.  The tokens' rows are not
+// copied into expert order; each is written once as f16, times a power of two
+// where f16's range asks for it.
 #pragma once
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cstdint>
 
-#include "schedule.cuh"
+#include "permute.cuh"
 #include "sm.cuh"
 #include "topk.cuh"
 
@@ -46,19 +49,25 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// E a multiple of 8, d of 16, T <= 16.  Grid: one cluster of kCtas.  tab
-// receives the experts in use (rows, first slot, expert; ascending).
+// E a multiple of 8, d of 16, T <= 16.  Grid: one cluster of kCtas.  units
+// [max_units] receives tiles of 8 rows of the experts in use (expert, first
+// slot, rows, 0), rows = 0 past the last.  x16 [T][d]: the rows in f16, each
+// divided by its scale (a power of two), which tokscale gets and gslot holds
+// with the gate.
 __global__ void __launch_bounds__(kThreads) route_group_kernel(
     const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ Wr, const float* __restrict__ bias, int T,
     int d, int E, int k, int32_t* __restrict__ idx, float* __restrict__ gate, float* __restrict__ lmax,
     float* __restrict__ margin, int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
-    int32_t* __restrict__ perm, float* __restrict__ gslot, GroupTable* tab) {
+    int32_t* __restrict__ perm, float* __restrict__ gslot, int4* __restrict__ units, int max_units,
+    __half* __restrict__ x16, float* __restrict__ tokscale) {
     op::pdl_enter();
     extern __shared__ __align__(128) uint8_t rg_smem[];
     __shared__ int32_t s_ent[kMaxEntries];   // selected expert of entry n = t * k + j (first CTA)
     __shared__ float s_gate[kMaxEntries];
     __shared__ int32_t s_rank[kMaxEntries];
     __shared__ int32_t s_rows[256], s_off[256];
+    __shared__ float s_scale[kTokens];       // first CTA: every token's scale
+    __shared__ float s_max[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x;
     const int nb = (E + kBlockCols - 1) / kBlockCols;  // 1 or 2 blocks of experts
@@ -66,6 +75,7 @@ __global__ void __launch_bounds__(kThreads) route_group_kernel(
     const int c0 = block * kBlockCols, cols = min(kBlockCols, E - c0);
     const int g = lane >> 2, t4 = lane & 3;
 
+    op::cluster_arrive();  // (the first CTA's shared memory is written below: it must have started)
     // ------------------------------------------------ this warp's share of the sums
     {
         uint8_t* ring = rg_smem + warp * kRing;
@@ -86,6 +96,29 @@ __global__ void __launch_bounds__(kThreads) route_group_kernel(
         };
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) issue(i);
+        op::cluster_wait();
+        // while they come: the rows of tokens rank and rank + 8 in f16
+        for (int t = rank; t < T; t += kCtas) {
+            const uint4* src = reinterpret_cast<const uint4*>(x + (size_t)t * d);
+            const int n = d / 8;
+            float m = 0.f;
+            for (int i = tid; i < n; i += kThreads) m = absmax_vec(src[i], m);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            __syncthreads();  // s_max has been read
+            if (lane == 0) s_max[warp] = m;
+            __syncthreads();
+            m = s_max[lane & (kWarps - 1)];
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float sc = f16_row_scale(m), r = 1.0f / sc;
+            for (int i = tid; i < n; i += kThreads)
+                reinterpret_cast<uint4*>(x16 + (size_t)t * d)[i] = cvt_row_vec(src[i], __nv_bfloat16{}, __half{}, r);
+            if (tid == 0) {
+                tokscale[t] = sc;
+                op::st_cluster_u32(op::mapa(op::smem_u32(s_scale + t), 0u), __float_as_uint(sc));
+            }
+        }
         float acc[kBlockCols / 8][4];
 #pragma unroll
         for (int i = 0; i < kBlockCols / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
@@ -226,24 +259,23 @@ __global__ void __launch_bounds__(kThreads) route_group_kernel(
             offsets[e] = off;
             counts[e] = rows;
         }
+        const unsigned big = __ballot_sync(0xffffffffu, rows > 8);  // (at most 16 rows: two tiles)
         if (rows > 0) {
-            const int at = used + __popc(some & ((1u << lane) - 1u));
-            tab->rows[at] = rows;
-            tab->row0[at] = off;
-            tab->expert[at] = e;
+            const unsigned lower = (1u << lane) - 1u;
+            const int at = used + __popc(some & lower) + __popc(big & lower);
+            units[at] = make_int4(e, off, min(rows, 8), 0);
+            if (rows > 8) units[at + 1] = make_int4(e, off + 8, rows - 8, 0);
         }
         base += __shfl_sync(0xffffffffu, incl, 31);
-        used += __popc(some);
+        used += __popc(some) + __popc(big);
     }
-    if (lane == 0) {
-        offsets[E] = base;
-        tab->num_groups = used;
-    }
+    for (int i = used + lane; i < max_units; i += 32) units[i] = make_int4(0, 0, 0, 0);
+    if (lane == 0) offsets[E] = base;
     __syncwarp();
     for (int n = lane; n < Tv; n += 32) {
         const int slot = s_off[s_ent[n]] + s_rank[n];
         perm[slot] = n;
-        gslot[slot] = s_gate[n];
+        gslot[slot] = s_gate[n] * s_scale[n / k];
     }
 }
 
