@@ -74,9 +74,11 @@ struct Cfg {
     static constexpr int XOFF = kRows * 64;
     static constexpr int SOFF = XOFF + NT8 * 8 * kXRow;
     static constexpr int STAGE = (SOFF + 2 * kCols * (int)sizeof(ST) + 1023) / 1024 * 1024;  // the swizzles' period
-    // three CTAs share an SM (168 registers a thread)
-    static constexpr int PER_SM = 3;
-    static constexpr int STAGES = NT8 == 1 ? 3 : 2;
+    // CTAs that share an SM: the registers' limit (up to 8 tokens 128 a
+    // thread, 16 tokens 168).  Four with two stages each beat three with
+    // three (1 x 5120 x 202048: 111 against 118 us): the arithmetic wants the warps
+    static constexpr int PER_SM = NT8 == 1 ? 4 : 3;
+    static constexpr int STAGES = 2;
     static constexpr int RING = STAGES * STAGE;
     static constexpr int RED = (int)sizeof(float) * kWarps * NT8 * 8 * kCols;  // over the rings
     static constexpr int SMEM = (kWarps * RING > RED ? kWarps * RING : RED) + 1024;  // and room to align them
@@ -284,28 +286,46 @@ __device__ __forceinline__ float find_factors(const Tokens<__nv_bfloat16>& X, in
     return mine;
 }
 
+// 16 bytes from any address of a matrix that ends at `end`: whole words,
+// shifted together, or byte by byte where those would reach past the end.
+__device__ __forceinline__ uint4 load_any16(const uint8_t* p, const uint8_t* end) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(a & ~uintptr_t(3));
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+    if (reinterpret_cast<const uint8_t*>(w + 5) <= end) {
+        uint32_t r[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) r[i] = __ldg(w + i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(r[i], r[i + 1], (uint32_t)(a & 3) * 8);
+    } else {
+#pragma unroll
+        for (int b = 0; b < 16; ++b)
+            if (p + b < end) v[b >> 2] |= (uint32_t)__ldg(p + b) << (8 * (b & 3));
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 // One stage's plain loads, for sizes that tensor maps do not take: lane l rows
-// l and l + 32 of the weight byte by byte, tokens and scales element by
-// element, zeros where nothing is (scales past N are not written: such
-// columns are not stored).
+// l and l + 32 of the weight (what lies past a row's end belongs to columns
+// that are not stored), tokens and scales element by element, zeros past K.
 template <int NT8, typename XT, typename ST>
 __device__ __forceinline__ void load_plain(uint8_t* stage, const Weight<ST>& W, int col0, const Tokens<XT>& X, int nt,
                                            int row, int end, bool s0, bool s1, int grp, int lane) {
     using Cf = Cfg<NT8, ST>;
-    const int nb = min(64, (W.N - col0) >> 1);  // N is even: whole bytes
+    const uint8_t* wend = W.q + (long long)W.K * (W.N / 2);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int r = lane + 32 * h;
         const uint8_t* p = W.q + (long long)(row + r) * (W.N / 2) + (col0 >> 1);
-        for (int c = 0; c < 4; ++c) {
-            uint32_t v[4] = {0u, 0u, 0u, 0u};
-            if (row + r < W.K) {
+        uint4 v[4];
 #pragma unroll
-                for (int b = 0; b < 16; ++b)
-                    if (c * 16 + b < nb) v[b >> 2] |= (uint32_t)__ldg(p + c * 16 + b) << (8 * (b & 3));
-            }
-            *reinterpret_cast<uint4*>(stage + chunk_at(r, c)) = make_uint4(v[0], v[1], v[2], v[3]);
+        for (int c = 0; c < 4; ++c) {
+            v[c] = make_uint4(0u, 0u, 0u, 0u);
+            if (row + r < W.K && col0 + 32 * c < W.N) v[c] = load_any16(p + 16 * c, wend);
         }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(stage + chunk_at(r, c)) = v[c];
     }
     for (int i = lane; i < nt * 8; i += 32) {
         const int t = i >> 3, c = i & 7;
