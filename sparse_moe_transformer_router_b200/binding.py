@@ -389,6 +389,8 @@ class L4MoE:
             raise ValueError(f"l4moe: x or out is not on the layer's device {self.device}")
         if out is None:
             out = x.new_empty((T, self.d_model))
+        if T == 0:  # (an empty tensor has no address to pass)
+            return out
         gu, dn = bound.arrays
         self._check(self._lib.l4moe_forward(self._h, T, _ptr(x), bound.router_ptr, gu, dn, bound.shared[0],
                                             bound.shared[1], _ptr(out), _stream_handle(stream)))

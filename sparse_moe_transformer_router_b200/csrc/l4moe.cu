@@ -1176,6 +1176,8 @@ l4moe_status l4moe_create(const l4moe_params* params, l4moe_handle** out) {
     h->sms = sms;
     h->h_maps.reserve(4 * (size_t)(p.num_experts + 1));
     h->scale_tab.assign(2 * (size_t)(p.num_experts + 1), nullptr);
+    for (auto* v : {&h->s_gu, &h->s_dn}) v->reserve((size_t)p.num_experts);
+    for (auto* v : {&h->key_gu, &h->key_dn, &h->hkey_gu, &h->hkey_dn}) v->reserve((size_t)p.num_experts);
     *out = h;
     return L4MOE_OK;
 }

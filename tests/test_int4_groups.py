@@ -394,16 +394,123 @@ def test_layer(d, F, Fs, E, k, group, st, tokens):
 
 
 @pytest.mark.gpu
-def test_layer_whose_tokens_all_take_one_expert():
-    m = Layer(128, 128, 64, 6, 32, "f32", k=2)
-    bias = torch.tensor([0.0, 0.0, 50.0, 0.0, 25.0, 0.0], device="cuda")
+@pytest.mark.parametrize("E", [6, 8])
+def test_layer_whose_tokens_all_take_one_expert(E):
+    m = Layer(128, 128, 64, E, 32, "f32", k=2)
+    bias = torch.zeros(E, device="cuda")
+    bias[2], bias[4] = 50.0, 25.0
     m.layer.set_router_bias(bias)
     for T in (16, 100):
         x = m.tokens(T)
         out = m.layer.forward(x, *m.weights())
         r = m.layer.routing()
-        assert r["counts"].tolist() == [0, 0, T, 0, T, 0]
+        assert r["counts"].tolist() == [0, 0, T, 0, T] + [0] * (E - 5)
+        assert r["offsets"].tolist() == [0, 0, 0, T, T] + [2 * T] * (E - 4)
+        assert r["perm"].view(2, T).tolist() == [list(range(0, 2 * T, 2)), list(range(1, 2 * T, 2))]
         m.check(out, x, r["idx"], r["gate"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,k,T", [(136, 4, 16), (256, 4, 16), (256, 1, 1), (8, 4, 9), (248, 2, 13), (128, 3, 16)])
+def test_layer_with_many_experts(E, k, T):
+    """More than 128 experts (two blocks of them in the routing), k up to 4."""
+    m = Layer(128, 64, 64, E, 64, "bf16", k=k)
+    x = m.tokens(T, seed=E)
+    m.run_and_check(x)
+    r = m.layer.routing()
+    idx = r["idx"].cpu().long()
+    assert torch.equal(r["counts"].cpu().long(), torch.bincount(idx, minlength=E))
+    assert torch.equal(r["perm"].cpu().long(), torch.argsort(idx, stable=True))
+    assert torch.equal(r["offsets"].cpu().long()[1:], torch.bincount(idx, minlength=E).cumsum(0))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E", [4, 8])
+def test_ties_and_nan_logits_route_as_the_layer_says(E):
+    """Equal logits take the lower index, NaN only when no number is left."""
+    m = Layer(64, 64, 64, E, 32, "f32", k=2)
+    zero = m.weights()
+    zero[0].zero_()
+    x = m.tokens(5)
+    m.layer.forward(x, *zero)
+    assert m.layer.routing()["idx"].tolist() == [0, 1] * 5
+    bias = torch.full((E,), float("nan"), device="cuda")
+    bias[3] = -float("inf")
+    m.layer.set_router_bias(bias)
+    m.layer.forward(x, *zero)
+    assert m.layer.routing()["idx"].tolist() == [3, 0] * 5
+
+
+@pytest.mark.gpu
+def test_tokens_past_f16s_range_and_not_finite_tokens():
+    """Rows of x beyond 65504 get a power of two; an infinite token is its own row's matter."""
+    m = Layer(128, 64, 64, 8, 32, "f16")
+    m.gu = [[w, s * 1e-6] for w, s in m.gu]
+    m.sgu = [m.sgu[0], m.sgu[1] * 1e-6]
+    m.gu, m.sgu = [[w, s.clamp(min=6e-8)] for w, s in m.gu], [m.sgu[0], m.sgu[1].clamp(min=6e-8)]
+    m.set_scales()
+    x = m.tokens(9)
+    x[::2] *= 2.0 ** 18
+    out = m.run_and_check(x)
+    x[3, 5] = float("inf")
+    bad = m.layer.forward(x, *m.weights())
+    keep = [0, 1, 2, 4, 5, 6, 7, 8]
+    assert torch.equal(bad[keep], out[keep]) and not bool(torch.isfinite(bad[3]).all())
+    with pytest.raises(L4MoEError):
+        m.layer.check_device_status()
+
+
+@pytest.mark.gpu
+def test_empty_batch_other_streams_and_two_layers_at_once():
+    a, b = Layer(256, 128, 128, 8, 64, "f16", seed=1), Layer(256, 192, 64, 16, 32, "bf16", k=2, seed=2)
+    assert a.layer.bind(*a.weights()).forward(a.tokens(0)).shape == (0, 256)
+    xa, xb = a.tokens(16), b.tokens(7)
+    want = a.run_and_check(xa), b.run_and_check(xb)
+    ba, bb = a.layer.bind(*a.weights()), b.layer.bind(*b.weights())
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [torch.empty_like(w) for w in want]
+    for _ in range(30):
+        ba.forward(xa, out=outs[0], stream=s1)
+        bb.forward(xb, out=outs[1], stream=s2.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+@pytest.mark.gpu
+def test_a_decode_step_with_its_router_watched_and_an_output_head():
+    """The three together: the layer's experts, the losses and counts of its
+    own routing, and a 4-bit output matrix, captured and replayed."""
+    from sparse_moe_transformer_router_b200.router_loss import router_loss
+    m = Layer(256, 128, 128, 16, 64, "f16", k=2)
+    bound = m.layer.bind(*m.weights())
+    g = torch.Generator().manual_seed(4)
+    head = [t.cuda() for t in quantize_int4_groups(torch.randn(256, 1024, generator=g) * 0.05, 64, torch.float16)]
+    x = m.tokens(12)
+    routing = None
+
+    def step():
+        h = bound.forward(x)
+        idx = m.layer.routing()["idx"]
+        r = router_loss(x.float() @ m.Wr.float(), 2, idx=idx)
+        return h, r, int4_matvec(h, head[0], head[1], 64)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h, r, logits = step()
+    for seed in (1, 2):
+        x.copy_(m.tokens(12, seed=seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        routing = m.layer.routing()
+        m.check(h, x, routing["idx"], routing["gate"])
+        check(logits, h, head[0], head[1], 64)
+        assert torch.equal(r.counts, routing["counts"]) and r.rows.item() == 12
+        f = routing["counts"].double() / 24
+        P = torch.softmax(x.double() @ m.Wr.double(), 1).mean(0)
+        assert abs(r.balance.item() - float(16 * (f * P).sum())) < 1e-4
 
 
 @pytest.mark.gpu

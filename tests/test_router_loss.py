@@ -384,6 +384,51 @@ def test_capture_and_replay(T):
 
 
 @pytest.mark.gpu
+def test_capture_of_the_gradient_through_autograd():
+    logits = make(200, 24, "f32", seed=3).requires_grad_()
+    torch.autograd.grad(router_loss(logits, 2, balance=0.5, z=0.25).loss, logits)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = router_loss(logits, 2, balance=0.5, z=0.25)
+        g, = torch.autograd.grad(2.0 * r.loss, logits)
+    with torch.no_grad():
+        logits.copy_(make(200, 24, "f32", seed=4))
+    graph.replay()
+    torch.cuda.synchronize()
+    check(router_loss(logits.detach(), 2, balance=0.5, z=0.25), reference(logits, 2, 0.5, 0.25), logits.detach(), 0.5,
+          0.25, up=2.0, grad=g)
+
+
+@pytest.mark.gpu
+def test_logits_changed_after_the_call_are_noticed_by_autograd():
+    leaf = make(20, 8, "f32").requires_grad_()
+    logits = leaf * 1.0
+    r = router_loss(logits, 1)
+    logits.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        r.loss.backward()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [700, 40000])
+def test_one_expert_and_padded_batches(T):
+    """E = 1, and a batch whose second half is padding (any size of launch)."""
+    one = make(T, 1, "f32")
+    check(router_loss(one, 1, balance=1.0, z=0.1), reference(one, 1, 1.0, 0.1), one, 1.0, 0.1)
+    logits = make(T, 20, "bf16", seed=1)
+    mask = torch.arange(T, device="cuda") < T // 2
+    logits[T // 2:] = math.nan
+    r = router_loss(logits, 2, balance=1.0, z=0.1, mask=mask)
+    half = router_loss(logits[:T // 2], 2, balance=1.0, z=0.1)
+    ref = reference(logits[:T // 2], 2, 1.0, 0.1)
+    check(half, ref, logits[:T // 2], 1.0, 0.1)
+    g = r.grad()
+    assert bool((g[T // 2:] == 0).all()) and torch.equal(r.counts, half.counts)
+    check(r, ref, logits[:T // 2], 1.0, 0.1, grad=g[:T // 2])
+
+
+@pytest.mark.gpu
 def test_counts_of_a_layers_routing():
     """The layer's own routing, read back and given: the counts are the layer's."""
     from sparse_moe_transformer_router_b200.binding import L4MoE
