@@ -27,8 +27,8 @@
 //   [0, 15] left where it lies in the f16's low bits is the subnormal u 2^-24
 //   (or 16 u 2^-24 one nibble up), exact in the tensor core.  No conversion
 //   instruction, 0.625 per weight in all.
-// - The bias 8 leaves as -8 sum(x) (2^-24) times the group's scale, once for
-//   each run of a group's blocks; the sums are two products with a constant.
+// - The bias 8 leaves through the sums' start value, -8 sum(x) (2^-24): two
+//   products with a constant per 32 rows, in the layout the others start from.
 // - The block's fp32 sum is multiplied by the group's scale and added to the
 //   column's total in fp32: the weights are never rounded to a product.
 // - Tokens come along in the ring, f16 rows as they are, bf16 rows divided (on
@@ -89,10 +89,10 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162flo
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                        uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                                        uint32_t b0, uint32_t b1, const float (&c)[4]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ void mma_f16_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                             uint32_t b0, uint32_t b1) {
@@ -147,11 +147,10 @@ __device__ __forceinline__ constexpr int tile_col(int i, int g) { return (i >> 1
 // acc += 32 rows of the warp's stage (rows_at: this lane's address of a matrix
 // load of the weight, x_at: of the tokens); sc: the scales of the lane's
 // columns; f: what the lane's tokens (column l / 4 of each 8) are multiplied
-// with as they become f16.  b8 += -8 2^-24 sum(x) of the lane's two tokens: a
-// product with rows of that constant (an f16 subnormal).
+// with as they become f16.  The sums start at -8 2^-24 sum(x): products of the
+// tokens with rows of that constant (an f16 subnormal).
 template <int NT8, bool BF>
-__device__ __forceinline__ void block_fma(float (&acc)[NT8][8][4], float (&b8)[NT8][4], uint32_t rows_at, uint32_t x_at,
-                                          const float (&sc)[16], const float (&f)[NT8]) {
+__device__ __forceinline__ void block_fma(float (&acc)[NT8][8][4], uint32_t rows_at, uint32_t x_at, const float (&sc)[16], const float (&f)[NT8]) {
     constexpr uint32_t kMinus8 = 0x80088008u;
     uint32_t b[NT8][4];
 #pragma unroll
@@ -165,6 +164,16 @@ __device__ __forceinline__ void block_fma(float (&acc)[NT8][8][4], float (&b8)[N
                 b[n][j] = *reinterpret_cast<const uint32_t*>(&h);
             }
         }
+    }
+    // the sums' start values (on even tiles, 16 times that on odd ones)
+    float c0[2][NT8][4];
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < NT8; ++n) {
+        mma_f16(c0[0][n], kMinus8, kMinus8, kMinus8, kMinus8, b[n][0], b[n][1], zero);
+        mma_f16_add(c0[0][n], kMinus8, kMinus8, kMinus8, kMinus8, b[n][2], b[n][3]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) c0[1][n][c] = 16.f * c0[0][n][c];
     }
 #pragma unroll
     for (int h = 0; h < 4; ++h) {  // columns 32 h .. 32 h + 31, four of them this lane's
@@ -183,7 +192,7 @@ __device__ __forceinline__ void block_fma(float (&acc)[NT8][8][4], float (&b8)[N
 #pragma unroll
             for (int n = 0; n < NT8; ++n) {
                 float d[4];
-                mma_f16(d, a[0], a[1], a[2], a[3], b[n][0], b[n][1]);
+                mma_f16(d, a[0], a[1], a[2], a[3], b[n][0], b[n][1], c0[s][n]);
                 mma_f16_add(d, a[4], a[5], a[6], a[7], b[n][2], b[n][3]);
                 float(&o)[4] = acc[n][2 * h + s];
                 o[0] = fmaf(sa, d[0], o[0]);
@@ -193,29 +202,6 @@ __device__ __forceinline__ void block_fma(float (&acc)[NT8][8][4], float (&b8)[N
             }
         }
     }
-#pragma unroll
-    for (int n = 0; n < NT8; ++n) {
-        mma_f16_add(b8[n], kMinus8, kMinus8, kMinus8, kMinus8, b[n][0], b[n][1]);
-        mma_f16_add(b8[n], kMinus8, kMinus8, kMinus8, kMinus8, b[n][2], b[n][3]);
-    }
-}
-
-// The bias of some blocks of one group: acc += scale * b8 (16 times that on
-// odd tiles).
-template <int NT8>
-__device__ __forceinline__ void bias_fma(float (&acc)[NT8][8][4], const float (&sc)[16], const float (&b8)[NT8][4]) {
-#pragma unroll
-    for (int n = 0; n < NT8; ++n)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float k = (i & 1) ? 16.f : 1.f, bx = k * b8[n][0], by = k * b8[n][1];
-            const float sa = sc[4 * (i >> 1) + (i & 1)], sb = sc[4 * (i >> 1) + (i & 1) + 2];
-            float(&o)[4] = acc[n][i];
-            o[0] = fmaf(sa, bx, o[0]);
-            o[1] = fmaf(sa, by, o[1]);
-            o[2] = fmaf(sb, bx, o[2]);
-            o[3] = fmaf(sb, by, o[3]);
-        }
 }
 
 // The f16 a value is staged as, and the power of two a bf16 row is
@@ -256,24 +242,29 @@ __device__ __forceinline__ float warp_max(float m) {
     return m;
 }
 
-// Lane tok: the factor of bf16 token tok over rows [r0, r1).  One warp, with
-// eight 16-byte loads of a lane on their way at once.
+// Lane tok: the factor of bf16 token tok over rows [r0, r1).  One warp; B: the
+// 16-byte loads of a lane (256 rows of a token each) on their way at once.
+template <int B>
 __device__ __forceinline__ float find_factors(const Tokens<__nv_bfloat16>& X, int nt, int r0, int r1, int lane) {
     const bool vec = (X.ld & 7) == 0;
-    const int rows = r1 - r0, per = (rows + 255) >> 8;  // loads of 256 rows per token
+    const int rows = r1 - r0, per = (rows + 255) >> 8;  // loads per token
+    const __nv_bfloat16* src = X.row(0) + r0;
     float mine = 1.f, m = 0.f;
-    int tok = 0, p = 0, tok_j = 0, p_j = 0;  // the next load's token and pass; the next one's to use
-    for (int i0 = 0; i0 < nt * per; i0 += 8) {
-        uint4 v[8];
+    int left = nt * per, p = 0, tok_j = 0, p_j = 0;  // loads left; the next load's pass; the next one's to use
+    while (left > 0) {
+        uint4 v[B];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < B; ++j) {
             v[j] = make_uint4(0u, 0u, 0u, 0u);
-            const int r = p * 256 + lane * 8;
-            if (tok < nt && r < rows) v[j] = load_x8(X.row(tok) + r0, r, rows, vec);
-            if (++p == per) p = 0, ++tok;
+            if (j < left) {
+                const int r = p * 256 + lane * 8;
+                if (r < rows) v[j] = load_x8(src, r, rows, vec);
+                if (++p == per) p = 0, src += X.ld;
+            }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < B; ++j) {
+            if (j >= left) break;
             m = absmax8(v[j], m);
             if (++p_j == per) {
                 m = warp_max(m);
@@ -282,6 +273,7 @@ __device__ __forceinline__ float find_factors(const Tokens<__nv_bfloat16>& X, in
                 p_j = 0, ++tok_j;
             }
         }
+        left -= B;
     }
     return mine;
 }
@@ -421,13 +413,13 @@ __device__ __forceinline__ bool warp_sums(uint8_t* ring, uint64_t* bar, float* r
 
     float factors = 1.f, f[NT8];
     if constexpr (BF) {
-        if (blocks > 0) factors = find_factors(X, nt, r0, r1, lane);
+        if (blocks > 0)
+            factors = nt * (r1 - r0) <= 512 ? find_factors<2>(X, nt, r0, r1, lane) : find_factors<8>(X, nt, r0, r1, lane);
     }
-    float acc[NT8][8][4], b8[NT8][4];  // b8: the bias not yet added, of the scales at hand
+    float acc[NT8][8][4];
 #pragma unroll
     for (int n = 0; n < NT8; ++n) {
         f[n] = __shfl_sync(0xffffffffu, factors, n * 8 + g);
-        b8[n][0] = b8[n][1] = b8[n][2] = b8[n][3] = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -455,7 +447,7 @@ __device__ __forceinline__ bool warp_sums(uint8_t* ring, uint64_t* bar, float* r
             for (int h = 0; h < 2; ++h) {
                 if (2 * (i0 + s) + h >= blocks) break;
                 if (left == 0) {  // a group's first rows bring its scales
-                    if (i0 + s + h > 0) bias_fma<NT8>(acc, sc, b8);
+                    
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         ST v[4];
@@ -463,13 +455,11 @@ __device__ __forceinline__ bool warp_sums(uint8_t* ring, uint64_t* bar, float* r
 #pragma unroll
                         for (int c = 0; c < 4; ++c) sc[4 * q + c] = to_f32(v[c]);
                     }
-#pragma unroll
-                    for (int n = 0; n < NT8; ++n) b8[n][0] = b8[n][1] = b8[n][2] = b8[n][3] = 0.f;
                     left = next;
                     next = W.group;
                 }
                 left -= kBlock;
-                block_fma<NT8, BF>(acc, b8, rows0 + s * Cf::STAGE + h * kBlock * 64,
+                block_fma<NT8, BF>(acc, rows0 + s * Cf::STAGE + h * kBlock * 64,
                                    (x0 + s * Cf::STAGE) ^ (h * 64), sc, f);
             }
             if (todo > 0) {
@@ -480,7 +470,6 @@ __device__ __forceinline__ bool warp_sums(uint8_t* ring, uint64_t* bar, float* r
             }
         }
     }
-    if (blocks > 0) bias_fma<NT8>(acc, sc, b8);
     if (TMA && !ok) {  // let what is on its way arrive before the memory is used again
         for (int s = 0; s < Cf::STAGES; ++s) op::mbar_wait(bar0 + s * 8, parity);
     }
