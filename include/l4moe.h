@@ -59,6 +59,9 @@
  *                   nibble: W_gate_up is [d, F] bytes, W_down [F, d/2] (same
  *                   for the shared expert); otherwise as L4MOE_INT8.
  *
+ *                   Instead of column scales, int4 layers may have one scale per
+ *                   group of input rows and output column (l4moe_set_group_scales).
+ *
  * Ownership: the caller owns every tensor, the scale vectors, the bias and
  * the stream.  The handle owns only its workspace (unless the caller supplies
  * one) and a cache of TMA descriptors keyed by the weight pointer values.

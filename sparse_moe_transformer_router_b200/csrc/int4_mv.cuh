@@ -19,23 +19,24 @@
 // - A warp takes 128 columns by 64 rows at a time through a ring of its own in
 //   shared memory, filled by TMA: one lane's few instructions bring the
 //   weight's box, the scales of the groups that begin there and the tokens'
-//   rows.  (As cp.async by every lane the copies cost as many issue slots as a
-//   third of the arithmetic: 113 us for 5120 x 202048 against what is noted
-//   below.)  The operand wants pairs along K: a transposing matrix load of 16-bit units, four
-//   columns each, returns two rows' units in one register.  Each pair of
-//   nibbles is then one AND (with the sign bit flipped) away: u = q + 8 in
-//   [0, 15] left where it lies in the f16's low bits is the subnormal u 2^-24
-//   (or 16 u 2^-24 one nibble up), exact in the tensor core.  No conversion
-//   instruction, 0.625 per weight in all.
+//   rows.  Copies issued by every lane (cp.async) took a quarter of the issue
+//   slots that the arithmetic wants (without the arithmetic, 5120 x 202048
+//   streams at 94% of the copy rate with TMA and 84% with cp.async).
+// - The operand wants pairs along K: a transposing matrix load of 16-bit
+//   units, four columns each, returns two rows' units in one register.  Each
+//   pair of nibbles is then one AND (with the sign bit flipped) away: u = q + 8
+//   in [0, 15] left where it lies in the f16's low bits is the subnormal u
+//   2^-24 (or 16 u 2^-24 one nibble up), exact in the tensor core.  No
+//   conversion instruction, 0.625 logic instructions per weight in all.
 // - The bias 8 leaves through the sums' start value, -8 sum(x) (2^-24): two
 //   products with a constant per 32 rows, in the layout the others start from.
 // - The block's fp32 sum is multiplied by the group's scale and added to the
 //   column's total in fp32: the weights are never rounded to a product.
-// - Tokens come along in the ring, f16 rows as they are, bf16 rows divided (on
-//   their way to the product) by a power of two that brings the largest of a
-//   warp's rows to [2^14, 2^15)
-//   (exact for values down to 2^-31 of it, others round at 2^-39 of it).
-//   A row with an infinity or a NaN gives NaN (inf times the bias).
+// - Tokens come along in the ring, f16 rows as they are, bf16 rows multiplied
+//   (on their way to the product) by a power of two that brings the largest of
+//   a warp's rows to [2^14, 2^15): exact for values down to 2^-31 of it, others
+//   round at 2^-39 of it.  A row with an infinity or a NaN gives NaN (inf times
+//   the bias).
 //
 // A CTA has four warps.  As an operator (and for the down product) it takes
 // 128 columns and a slice of K, each warp a quarter of the slice; for gate/up
@@ -44,6 +45,15 @@
 // through shared memory and the slices of a cluster through distributed shared
 // memory, always in the same order.  Every wait for a copy gives up after a
 // second: the sums become NaN (and the layer's error word gets a bit).
+//
+// What bounds it: a scheduler issues a logic instruction every other cycle and
+// an m16n8k16 product every eight, and per 32 rows x 128 columns a warp needs
+// 80 and 18 of them beside 32 fp32 FMAs, about 300 cycles where HBM delivers
+// the bytes in 260.  Measured on one B200 (device time, three weights in turn):
+//   1 x 5120 x 202048, groups of 128   110 us   4.8 TB/s   0.74 of the copy rate
+//   1 x 5120 x 16384                    16 us   2.7 TB/s   (4 us of it launch, first loads, joining)
+//   16 x 8192 x 5120, groups of 64      15 us   1.5 TB/s   (two token columns: twice the products)
+// The layer's figures stand at experts_kernel.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -623,6 +633,15 @@ __device__ __forceinline__ int2 find_unit(const GroupTable* tab, int u) {
 // Gate/up: h = silu(c a_gate) (c a_up), c the row's scale (its sigmoid gate).
 // Down: the fp32 sums, un-permuted.  Grid: (column tiles, units, slices); a
 // tile is 128 hidden columns (gate/up) or 128 columns (down).
+//
+// Bound like the operator: by the weights' bytes, then by the logic that
+// widens them.  8 rows of an expert at a time, so a unit is a column of
+// products; more rows of one expert read its weights again, from L2 when they
+// are taken side by side.  Layer of width 5120 and 8192, one B200, device time
+// of a whole forward: one token, 128 experts, groups of 128: 53 us (131 MB,
+// 2.5 TB/s; routing 9 us of it, which the shared expert's gate/up overlaps);
+// sixteen tokens, 16 experts, groups of 32: 198 us (800 MB, 4.05 TB/s; a scale
+// per 32 rows and column adds a fifth to the arithmetic).
 template <typename ST, bool GATE_UP>
 __global__ void __launch_bounds__(kThreads, Cfg<1, ST>::PER_SM) experts_kernel(const __grid_constant__ Rows R) {
     extern __shared__ __align__(16) uint8_t mv_smem[];

@@ -12,6 +12,12 @@
 // makes the slots.  All sums in a fixed order.  The tokens' rows are not
 // copied into expert order; each is written once as f16, times a power of two
 // where f16's range asks for it.
+//
+// About 9 us for one token, d 5120, 128 experts (1.3 MB of W_router; the floor
+// is 0.2 us: it is the chain of launch, first loads, three cluster barriers
+// and the slots).  The one-launch routing of the other layers, whose last CTA
+// converts and copies every row alone, took 35 us there and 83 us with sixteen
+// tokens.  8 CTAs: 16 (the non-portable cluster size) would not shorten the chain.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

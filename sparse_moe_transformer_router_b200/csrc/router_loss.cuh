@@ -22,8 +22,15 @@
 // gradient's write) for long batches and by the launches for short ones.  A
 // row is spread over L lanes of a warp, 8 neighbouring experts to a lane (one
 // 16-byte load of a 16-bit row), so its sums and choices are butterflies of
-// log2 L shuffles and small rows share a warp.  Sums are fp32 in a lane and a
-// block, 64-bit across blocks, always in the same order.
+// log2 L shuffles and small rows share a warp.  Sums are fp32, always in the
+// same order.
+//
+// For long rows the arithmetic bounds both: about 350 instructions per row of
+// 256 (exponentials, reciprocals, keys and choices) where HBM delivers the 512
+// bytes in the time of 90.  Measured on one B200 (device time of values and
+// gradient together): 65536 x 256 bf16, sigmoid, four choices: 59 us (values
+// 34, gradient 23); 16384 x 128 fp32 18 us; 4096 x 16 bf16 7 us and 64 x 4 fp32
+// 5 us (two launches).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
