@@ -19,9 +19,9 @@
 // - A warp takes 128 columns by 64 rows at a time through a ring of its own in
 //   shared memory, filled by TMA: one lane's few instructions bring the
 //   weight's box, the scales of the groups that begin there and the tokens'
-//   rows.  Copies issued by every lane (cp.async) took a quarter of the issue
-//   slots that the arithmetic wants (without the arithmetic, 5120 x 202048
-//   streams at 94% of the copy rate with TMA and 84% with cp.async).
+//   rows.  Copies issued by every lane (cp.async) compete with the arithmetic
+//   for issue slots: with the arithmetic taken out, 5120 x 202048 streams in
+//   87 us by TMA and in 95 to 97 by cp.async (floor 81).
 // - The operand wants pairs along K: a transposing matrix load of 16-bit
 //   units, four columns each, returns two rows' units in one register.  Each
 //   pair of nibbles is then one AND (with the sign bit flipped) away: u = q + 8
@@ -46,12 +46,14 @@
 // memory, always in the same order.  Every wait for a copy gives up after a
 // second: the sums become NaN (and the layer's error word gets a bit).
 //
-// What bounds it: a scheduler issues a logic instruction every other cycle and
-// an m16n8k16 product every eight, and per 32 rows x 128 columns a warp needs
-// 80 and 18 of them beside 32 fp32 FMAs, about 300 cycles where HBM delivers
-// the bytes in 260.  Measured on one B200 (device time, three weights in turn):
+// What bounds it: loads and arithmetic of nearly the same length that overlap
+// in part.  5120 x 202048 takes 87 us with the arithmetic taken out, 97 with
+// the loads taken out, 110 together.  A scheduler issues a logic instruction
+// every other cycle and an m16n8k16 product every eight (measured), and per 32
+// rows x 128 columns a warp needs 80 and 18 of them beside 32 fp32 FMAs.
+// Measured on one B200 (device time, three weights in turn):
 //   1 x 5120 x 202048, groups of 128   110 us   4.8 TB/s   0.74 of the copy rate
-//   1 x 5120 x 16384                    16 us   2.7 TB/s   (4 us of it launch, first loads, joining)
+//   1 x 5120 x 16384                    16 us   2.7 TB/s   (1 x 512 x 128 alone takes 3.9 us)
 //   16 x 8192 x 5120, groups of 64      15 us   1.5 TB/s   (two token columns: twice the products)
 // The layer's figures stand at experts_kernel.
 #pragma once
@@ -635,13 +637,12 @@ __device__ __forceinline__ int2 find_unit(const GroupTable* tab, int u) {
 // tile is 128 hidden columns (gate/up) or 128 columns (down).
 //
 // Bound like the operator: by the weights' bytes, then by the logic that
-// widens them.  8 rows of an expert at a time, so a unit is a column of
-// products; more rows of one expert read its weights again, from L2 when they
-// are taken side by side.  Layer of width 5120 and 8192, one B200, device time
+// widens them.  8 rows of an expert at a time; more rows of one expert
+// read its weights again.  Layer of width 5120 and 8192, one B200, device time
 // of a whole forward: one token, 128 experts, groups of 128: 53 us (131 MB,
-// 2.5 TB/s; routing 9 us of it, which the shared expert's gate/up overlaps);
-// sixteen tokens, 16 experts, groups of 32: 198 us (800 MB, 4.05 TB/s; a scale
-// per 32 rows and column adds a fifth to the arithmetic).
+// 2.5 TB/s); sixteen tokens, 16 experts, groups of 32: 198 to 201 us (800 MB,
+// 4.0 TB/s).  Between events, which keep the launches from overlapping:
+// routing 17, gate/up 29, down 23 us and 15, 127, 72 us.
 template <typename ST, bool GATE_UP>
 __global__ void __launch_bounds__(kThreads, Cfg<1, ST>::PER_SM) experts_kernel(const __grid_constant__ Rows R) {
     extern __shared__ __align__(16) uint8_t mv_smem[];

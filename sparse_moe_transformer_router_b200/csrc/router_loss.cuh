@@ -25,11 +25,12 @@
 // log2 L shuffles and small rows share a warp.  Sums are fp32, always in the
 // same order.
 //
-// For long rows the arithmetic bounds both: about 350 instructions per row of
-// 256 (exponentials, reciprocals, keys and choices) where HBM delivers the 512
-// bytes in the time of 90.  Measured on one B200 (device time of values and
-// gradient together): 65536 x 256 bf16, sigmoid, four choices: 59 us (values
-// 34, gradient 23); 16384 x 128 fp32 18 us; 4096 x 16 bf16 7 us and 64 x 4 fp32
+// For long rows the arithmetic bounds both: 366 warp instructions per row
+// of 256 in the values' pass (counted by a profiler for sigmoid and four
+// choices: exponentials, reciprocals, keys and choices), where HBM delivers the
+// 512 bytes in about 90 cycles of a scheduler.  Measured on one B200 (device time of values and
+// gradient together): 65536 x 256 bf16, sigmoid, four choices: 59 to
+// 60 us; 16384 x 128 fp32 18 us; 4096 x 16 bf16 7 us and 64 x 4 fp32
 // 5 us (two launches).
 #pragma once
 #include <cuda_bf16.h>
