@@ -167,6 +167,8 @@ def _where(t, name, host=False):
         raise ValueError(f"l4moe: {name} must be a {'host' if host else 'CUDA'} tensor")
 
 
+MAX_INT = 2 ** 31 - 1  # of the library's int arguments (ctypes would wrap a larger value)
+
 # element types of the operators that take no handle (l4moe_elem)
 ELEMS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
@@ -293,8 +295,8 @@ class L4MoE:
     def _set_group_scales(self, s_gate_up, s_down, ss_gate_up, ss_down, group):
         if self.dtype != "int4":
             raise ValueError(f"l4moe: group scales apply to int4 weights, not {self.dtype}")
-        if group < 32 or group % 32:
-            raise ValueError(f"l4moe: group = {group}, expected a multiple of 32")
+        if group < 32 or group % 32 or group > MAX_INT:
+            raise ValueError(f"l4moe: group = {group}, expected a multiple of 32 below 2^31")
         d, F, Fs, E = self.d_model, self.expert_ffn, self.shared_ffn, self.num_experts
         if len(s_gate_up) != E or len(s_down) != E:
             raise ValueError(f"l4moe: expected scales of {E} experts, got {len(s_gate_up)} / {len(s_down)}")

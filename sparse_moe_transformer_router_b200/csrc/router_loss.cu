@@ -166,6 +166,7 @@ l4moe_status l4moe_router_loss(int T, int E, int k, const void* logits, l4moe_el
     l4moe_status s = check_logits("l4moe_router_loss", T, E, logits, type, ld, score);
     if (s != L4MOE_OK) return s;
     if (k < 1 || k > kLossMaxK || k > E) return op_fail(L4MOE_ERR_ARG, "l4moe_router_loss: k must be in [1, min(4, E)]");
+    if ((long long)T * k > INT32_MAX) return op_fail(L4MOE_ERR_ARG, "l4moe_router_loss: T k above 2^31 - 1 (32-bit counts)");
     if (!result || !workspace) return op_fail(L4MOE_ERR_ARG, "l4moe_router_loss: null result or workspace");
     if ((reinterpret_cast<uintptr_t>(result) | reinterpret_cast<uintptr_t>(workspace) |
          reinterpret_cast<uintptr_t>(idx)) & 3u)

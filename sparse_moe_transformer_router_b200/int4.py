@@ -15,9 +15,10 @@ from __future__ import annotations
 
 import torch
 
-from .binding import ELEMS, check_op, load_library, op_stream
+from .binding import ELEMS, MAX_INT, check_op, load_library, op_stream
 
 MAX_TOKENS = 64
+MAX_SIDE = 1 << 30  # of K and N
 _X_TYPES = (torch.bfloat16, torch.float16)
 
 
@@ -33,8 +34,10 @@ def _refuse(x, w, scales, group, out):
         raise ValueError(f"l4moe: w has dtype {w.dtype}, expected uint8")
     if scales.dtype not in ELEMS:
         raise ValueError(f"l4moe: scales have dtype {scales.dtype}, expected float32, bfloat16 or float16")
-    if group < 32 or group % 32:
-        raise ValueError(f"l4moe: group = {group}, expected a multiple of 32")
+    if group < 32 or group % 32 or group > MAX_INT:
+        raise ValueError(f"l4moe: group = {group}, expected a multiple of 32 below 2^31")
+    if K > MAX_SIDE or N > MAX_SIDE:
+        raise ValueError(f"l4moe: K = {K}, N = {N}, expected at most {MAX_SIDE}")
     if T > MAX_TOKENS:
         raise ValueError(f"l4moe: {T} tokens, expected at most {MAX_TOKENS}")
     if K < 1 or N < 2 or w.shape[0] != K:
@@ -60,8 +63,8 @@ def _accepts(x, w, scales, group, out, T, K, N):
     """The conditions of `_refuse` in one pass (a call of a few microseconds
     pays for every look at a tensor)."""
     dev = x.get_device()
-    return (x.dtype in _X_TYPES and w.dtype is torch.uint8 and scales.dtype in ELEMS and group >= 32
-            and group % 32 == 0 and T <= MAX_TOKENS and K >= 1 and N >= 2 and w.shape == (K, N // 2)
+    return (x.dtype in _X_TYPES and w.dtype is torch.uint8 and scales.dtype in ELEMS and 32 <= group <= MAX_INT
+            and group % 32 == 0 and T <= MAX_TOKENS and 1 <= K <= MAX_SIDE and 2 <= N <= MAX_SIDE and w.shape == (K, N // 2)
             and scales.shape == (-(-K // group), N) and dev >= 0 and w.get_device() == dev
             and scales.get_device() == dev and x.is_contiguous() and w.is_contiguous() and scales.is_contiguous()
             and (out is None or (out.shape == (T, N) and out.dtype is x.dtype and out.get_device() == dev

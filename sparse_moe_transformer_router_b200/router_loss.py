@@ -31,7 +31,7 @@ import functools
 
 import torch
 
-from .binding import ELEMS, check_op, load_library, op_stream
+from .binding import ELEMS, MAX_INT, check_op, load_library, op_stream
 
 SCORES = {"softmax": 0, "sigmoid": 1}
 MAX_EXPERTS = 256
@@ -45,7 +45,7 @@ def _accepts(logits, k, score, mask, idx):
         return False
     T, E = logits.shape
     dev = logits.get_device()
-    return (logits.dtype in ELEMS and 1 <= E <= MAX_EXPERTS and 1 <= k <= MAX_K and k <= E and score in SCORES
+    return (logits.dtype in ELEMS and 1 <= E <= MAX_EXPERTS and 1 <= k <= MAX_K and k <= E and T * k <= MAX_INT and score in SCORES
             and dev >= 0 and logits.is_contiguous()
             and (mask is None or (mask.shape == (T,) and mask.dtype is torch.bool and mask.get_device() == dev
                                   and mask.is_contiguous()))
@@ -65,6 +65,8 @@ def _refuse(logits, k, score, mask, idx):
         raise ValueError(f"l4moe: {E} experts, expected 1 to {MAX_EXPERTS}")
     if not 1 <= k <= min(MAX_K, E):
         raise ValueError(f"l4moe: k = {k}, expected 1 to {min(MAX_K, E)}")
+    if T * k > MAX_INT:  # (the counts are 32-bit)
+        raise ValueError(f"l4moe: {T} rows of {k} choices, expected fewer than 2^31 in all")
     if score not in SCORES:
         raise ValueError(f"l4moe: unknown score {score!r}")
     _rows(logits, "logits")

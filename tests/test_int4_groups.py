@@ -87,6 +87,22 @@ def test_refusals_of_the_binding():
             int4_matvec(*args)
 
 
+def test_sizes_past_the_librarys_integers_are_refused():
+    x, w, s = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(64, 16, dtype=torch.uint8), torch.zeros(1, 32)
+    for group in (2 ** 31, 2 ** 32 + 32):  # the second would reach the library as 32
+        with pytest.raises(ValueError, match="group"):
+            int4_matvec(x, w, s, group)
+    N = 2 ** 32 + 32
+    wide = torch.empty((1, N // 2), dtype=torch.uint8, device="meta")
+    with pytest.raises(ValueError, match="at most"):
+        int4_matvec(torch.empty((1, 1), dtype=torch.bfloat16, device="meta"), wide,
+                    torch.empty((1, N), device="meta"), 32)
+    layer = object.__new__(L4MoE)
+    layer.dtype = "int4"
+    with pytest.raises(ValueError, match="group"):
+        layer.set_weight_scales([], [], None, None, group=2 ** 32 + 32)
+
+
 def test_refusals_of_the_library():
     lib = binding.load_library()
     A = 256

@@ -113,6 +113,14 @@ def test_refusals_of_the_binding():
             router_loss(bad, **kw)
 
 
+def test_batches_past_32_bit_counts_are_refused():
+    for T, k in ((2 ** 31, 1), (2 ** 32 + 4, 1), (2 ** 30, 2)):
+        with pytest.raises(ValueError, match="choices"):
+            router_loss(torch.empty((T, 2), dtype=torch.bfloat16, device="meta"), k)
+    lib = binding.load_library()
+    assert lib.l4moe_router_loss(2 ** 30, 8, 2, 256, 0, 8, None, None, 0, 1.0, 1.0, 256, 256, 0, None) == binding.ERR_ARG
+
+
 def test_refusals_of_the_library():
     lib = binding.load_library()
     A = 256  # a pointer value that no refused call follows
