@@ -422,8 +422,8 @@ L4MOE_API l4moe_status l4moe_router_loss_grad(int T, int E, const void *logits, 
  * is taken exactly; bf16 rows are divided by a power of two into f16's range,
  * exact down to 2^-31 of the row's largest magnitude and to 2^-39 of it
  * below.  A row of x with an infinity or a NaN gives NaN in all its outputs;
- * the other rows are not touched by it.  w need not differ between calls in
- * flight; tensors 16-byte aligned, contiguous, on the current device. */
+ * the other rows are not touched by it.  y must not overlap an input; w need
+ * not differ between calls in flight; tensors 16-byte aligned, contiguous, on the current device. */
 #define L4MOE_INT4_MAX_TOKENS 64
 L4MOE_API l4moe_status l4moe_int4_matvec(int T, int K, int N, int group, const void *x, l4moe_elem x_type,
                                const void *w, const void *scales, l4moe_elem s_type, void *y,

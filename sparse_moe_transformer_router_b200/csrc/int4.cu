@@ -80,6 +80,11 @@ extern "C" l4moe_status l4moe_int4_matvec(int T, int K, int N, int group, const 
     if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(scales) |
          reinterpret_cast<uintptr_t>(y)) & 15u)
         return op_fail(L4MOE_ERR_ALIGN, "l4moe_int4_matvec: tensor pointer not 16-byte aligned");
+    // the output is written while other CTAs still read the inputs
+    const size_t xb = (size_t)T * K * 2, wb = (size_t)K * (N / 2), yb = (size_t)T * N * 2;
+    const size_t sb = ((size_t)K + group - 1) / group * N * (s_type == L4MOE_ELEM_F32 ? 4 : 2);
+    if (overlap(y, yb, x, xb) || overlap(y, yb, w, wb) || overlap(y, yb, scales, sb))
+        return op_fail(L4MOE_ERR_ARG, "l4moe_int4_matvec: y overlaps an input");
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

@@ -13,6 +13,12 @@
 
 namespace l4moe {
 
+// Whether a bytes at p and b bytes at q share any.
+inline bool overlap(const void* p, size_t a, const void* q, size_t b) {
+    const uintptr_t u = reinterpret_cast<uintptr_t>(p), v = reinterpret_cast<uintptr_t>(q);
+    return u < v + b && v < u + a;
+}
+
 // Record msg for l4moe_last_error(NULL) (this thread's) and return s.
 l4moe_status op_fail(l4moe_status s, const char* msg) noexcept;
 

@@ -45,6 +45,18 @@ l4moe_status cuda_error(cudaError_t e, const char* what) {
 
 size_t elem_bytes(l4moe_elem t) { return t == L4MOE_ELEM_F32 ? 4 : 2; }
 
+// Whether rows of E elements at p (ld apart) and q (ldd apart) may share
+// memory: their ranges do, unless both are columns of one matrix that lie
+// side by side.
+bool rows_overlap(int T, int E, const void* p, long long ld, const void* q, long long ldd, size_t size) {
+    const size_t n = (size_t)E * size, a = (size_t)(T - 1) * ld * size, b = (size_t)(T - 1) * ldd * size;
+    if (!overlap(p, a + n, q, b + n)) return false;
+    if (ld != ldd) return true;
+    const uintptr_t u = reinterpret_cast<uintptr_t>(p), v = reinterpret_cast<uintptr_t>(q);
+    const size_t pitch = (size_t)ld * size, at = (u > v ? u - v : v - u) % pitch;
+    return at < n || at > pitch - n;
+}
+
 // What both entry points ask of the logits.
 l4moe_status check_logits(const char* fn, int T, int E, const void* logits, l4moe_elem type, long long ld,
                           l4moe_score score) {
@@ -193,6 +205,8 @@ l4moe_status l4moe_router_loss_grad(int T, int E, const void* logits, l4moe_elem
         ((reinterpret_cast<uintptr_t>(result) | reinterpret_cast<uintptr_t>(upstream)) & 3u))
         return op_fail(L4MOE_ERR_ALIGN, "l4moe_router_loss_grad: misaligned pointer");
     if (T == 0) return L4MOE_OK;
+    if (rows_overlap(T, E, logits, ld, dlogits, ldd, elem_bytes(type)))
+        return op_fail(L4MOE_ERR_ARG, "l4moe_router_loss_grad: dlogits overlaps the logits");
     const int sms = device_sms();
     if (sms < 1) return op_fail(L4MOE_ERR_CUDA, "l4moe_router_loss_grad: no CUDA device");
     const long long rows = (long long)(kGradThreads / 32) * (32 / lanes_of(E));

@@ -123,6 +123,14 @@ def test_refusals_of_the_library():
     assert lib.l4moe_set_group_scales(None, 32, 0, None, None, None, None) == binding.ERR_ARG
 
 
+def test_outputs_over_inputs_are_refused():
+    lib = binding.load_library()
+    at = {"x": 1 << 20, "w": 2 << 20, "s": 3 << 20}  # never followed
+    for over in at.values():
+        for y in (over, over + 16, over - 16):  # y: 2 x 64 bf16, 256 bytes
+            assert lib.l4moe_int4_matvec(2, 64, 64, 32, at["x"], 1, at["w"], at["s"], 0, y, None) == binding.ERR_ARG
+
+
 def test_refusals_of_group_scales():
     layer = object.__new__(L4MoE)  # no library call: only the host-side checks
     layer.d_model, layer.expert_ffn, layer.shared_ffn, layer.num_experts, layer.dtype = 64, 128, 192, 2, "int4"

@@ -121,6 +121,22 @@ def test_batches_past_32_bit_counts_are_refused():
     assert lib.l4moe_router_loss(2 ** 30, 8, 2, 256, 0, 8, None, None, 0, 1.0, 1.0, 256, 256, 0, None) == binding.ERR_ARG
 
 
+def test_a_gradient_over_its_logits_is_refused():
+    lib = binding.load_library()
+
+    def grad(dl, ld=8, ldd=8, T=4):
+        return lib.l4moe_router_loss_grad(T, 8, 1 << 20, 0, ld, None, 0, 256, None, dl, ldd, None)
+
+    A = 1 << 20
+    for kw in ({"dl": A}, {"dl": A + 32}, {"dl": A - 96}, {"dl": A + 12, "ld": 20, "ldd": 20},
+               {"dl": A + 32, "ld": 16, "ldd": 8}, {"dl": A + 52, "ld": 16, "ldd": 16}):
+        assert grad(**kw) == binding.ERR_ARG, kw
+        assert b"overlaps" in lib.l4moe_last_error(None)
+    if not torch.cuda.is_available():  # columns side by side, and rows that follow: as far as the missing device
+        for kw in ({"dl": A + 32, "ld": 16, "ldd": 16}, {"dl": A - 32, "ld": 16, "ldd": 16}, {"dl": A + 128}):
+            assert grad(**kw) == binding.ERR_CUDA, kw
+
+
 def test_refusals_of_the_library():
     lib = binding.load_library()
     A = 256  # a pointer value that no refused call follows
