@@ -156,18 +156,18 @@ class _Loss(torch.autograd.Function):
     """The loss as a function of the logits."""
 
     @staticmethod
-    def forward(ctx, logits, args, box):
+    def forward(ctx, logits, mask, args, box):
         r = _forward(logits.detach(), *args)
         box.append(r)
-        ctx.save_for_backward(logits, r._result)
-        ctx.mask, ctx.score = r._mask, r._score
+        ctx.save_for_backward(logits, r._result, mask)
+        ctx.score = r._score
         return r.loss.clone()
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, upstream):
-        logits, result = ctx.saved_tensors
-        return RouterLoss(logits.detach(), ctx.mask, ctx.score, result).grad(upstream.contiguous()), None, None
+        logits, result, mask = ctx.saved_tensors
+        return RouterLoss(logits.detach(), mask, ctx.score, result).grad(upstream.contiguous()), None, None, None
 
 
 def router_loss(logits: torch.Tensor, k: int = 1, *, balance: float = 1e-2, z: float = 1e-3, score: str = "softmax",
@@ -186,7 +186,7 @@ def router_loss(logits: torch.Tensor, k: int = 1, *, balance: float = 1e-2, z: f
     if not (logits.requires_grad and torch.is_grad_enabled()):
         return _forward(logits, *args)
     box = []
-    loss = _Loss.apply(logits, args, box)
+    loss = _Loss.apply(logits, mask, args, box)
     r = box[0]
     r.loss = loss
     return r

@@ -435,6 +435,16 @@ def test_logits_changed_after_the_call_are_noticed_by_autograd():
 
 
 @pytest.mark.gpu
+def test_a_mask_changed_after_the_call_is_noticed_by_autograd():
+    logits = make(20, 8, "f32").requires_grad_()
+    mask = torch.ones(20, dtype=torch.bool, device="cuda")
+    r = router_loss(logits, 1, mask=mask)
+    mask[3] = False
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        r.loss.backward()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [700, 40000])
 def test_one_expert_and_padded_batches(T):
     """E = 1, and a batch whose second half is padding (any size of launch)."""
