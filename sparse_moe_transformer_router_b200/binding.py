@@ -182,18 +182,23 @@ def check_op(st: int):
 class _Elsewhere:
     """Runs an operator on another device or stream than the current ones:
     both are current inside, so buffers allocated there belong to the stream
-    that uses them."""
+    that uses them.  The memory of the tensors `used` is not given out again
+    before the stream's work so far has run."""
 
-    def __init__(self, device, stream):
+    def __init__(self, device, stream, used=()):
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
         if stream is not None and stream.device != device:
             raise ValueError(f"l4moe: stream of {stream.device}, tensors on {device}")
         self._scope = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
-        self._device, self._stream = device, stream
+        self._device, self._stream, self._used = device, stream, used
 
     def __enter__(self):
         self._scope.__enter__()
+        if self._stream is not None:
+            for t in self._used:
+                if t is not None:
+                    t.record_stream(self._stream)
         return (self._stream or torch.cuda.current_stream(self._device)).cuda_stream
 
     def __exit__(self, *exc):
@@ -213,15 +218,15 @@ class _Here:
         return None
 
 
-def op_stream(tensor, stream):
+def op_stream(tensor, stream, *used):
     """Context of one operator call on `tensor`'s device and on `stream` (a
-    torch stream or a raw handle; None: that device's current one).  Gives the
-    raw handle."""
+    torch stream or a raw handle; None: that device's current one), with the
+    tensors (or None) that it reads or writes.  Gives the raw handle."""
     if stream is None:
         index = tensor.get_device()
         if index == _current_device():
             return _Here(_raw_stream(index))
-    return _Elsewhere(tensor.device, stream)
+    return _Elsewhere(tensor.device, stream, used)
 
 
 class _DevView:
@@ -389,13 +394,14 @@ class L4MoE:
         T = self._check_io(x, bound.W_router, out)
         if x.get_device() != self.device.index or (out is not None and out.get_device() != self.device.index):
             raise ValueError(f"l4moe: x or out is not on the layer's device {self.device}")
-        if out is None:
-            out = x.new_empty((T, self.d_model))
-        if T == 0:  # (an empty tensor has no address to pass)
-            return out
         gu, dn = bound.arrays
-        self._check(self._lib.l4moe_forward(self._h, T, _ptr(x), bound.router_ptr, gu, dn, bound.shared[0],
-                                            bound.shared[1], _ptr(out), _stream_handle(stream)))
+        with op_stream(x, stream, x, out) as st:
+            if out is None:
+                out = x.new_empty((T, self.d_model))
+            if T == 0:  # (an empty tensor has no address to pass)
+                return out
+            self._check(self._lib.l4moe_forward(self._h, T, _ptr(x), bound.router_ptr, gu, dn, bound.shared[0],
+                                                bound.shared[1], _ptr(out), st))
         self.last_T = T
         return out
 

@@ -82,7 +82,7 @@ def int4_matvec(x: torch.Tensor, w: torch.Tensor, scales: torch.Tensor, group: i
     if not _accepts(x, w, scales, group, out, T, K, N):
         _refuse(x, w, scales, group, out)
         raise ValueError("l4moe: int4_matvec does not take these arguments")
-    with op_stream(x, stream) as st:
+    with op_stream(x, stream, x, w, scales, out) as st:
         if out is None:
             out = x.new_empty((T, N))
         check_op(_call()(T, K, N, group, x.data_ptr(), ELEMS[x.dtype], w.data_ptr(), scales.data_ptr(),

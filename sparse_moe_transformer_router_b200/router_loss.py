@@ -21,7 +21,9 @@ with dropped entries (any index outside [0, E)).
 
 Where the logits take part in autograd (a leaf or the output of the router's
 product), `r.loss` has their gradient: `(task_loss + r.loss).backward()`.
-The other values carry none.  One pass reads the logits for the values, one
+The other values carry none.  Before a backward pass is captured into a CUDA
+graph, let go of eager losses of the same leaves, as for any torch function.
+One pass reads the logits for the values, one
 more for the gradient; everything runs in the library's CUDA kernels on the
 caller's stream, with no host synchronisation.
 """
@@ -99,8 +101,9 @@ def _stride(t):
 class RouterLoss:
     """The values of one `router_loss` call (views of one device buffer)."""
 
-    def __init__(self, logits, mask, score, result):
+    def __init__(self, logits, mask, score, result, home):
         self._logits, self._mask, self._score, self._result = logits, mask, score, result
+        self._home = home  # the stream (raw handle) that the result's memory belongs to
         self.loss, self.balance, self.z, self.rows = result[:4].unbind()
 
     @property
@@ -109,8 +112,9 @@ class RouterLoss:
 
     def grad(self, upstream: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """The gradient of the logits, times `upstream` (an fp32 device
-        scalar; None: 1), in the logits' type.  `out`: where to write it.
-        The logits (and the mask) must still hold what the call read."""
+        scalar; None: 1), in the logits' type.  `out`: where to write it (not
+        over the logits).  The logits (and the mask) must still hold what the
+        call read, and the stream must have waited for the call's."""
         logits = self._logits
         T, E = logits.shape
         if upstream is not None:
@@ -121,7 +125,9 @@ class RouterLoss:
             if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
                 raise ValueError("l4moe: out must have the logits' shape, dtype and device")
             _rows(out, "out")
-        with op_stream(logits, stream) as st:
+        with op_stream(logits, stream, logits, self._mask, upstream, out) as st:
+            if st != self._home:
+                self._result.record_stream(torch.cuda.current_stream(logits.device))
             if out is None:
                 out = logits.new_empty((T, E))
             check_op(load_library().l4moe_router_loss_grad(
@@ -140,7 +146,7 @@ def _workspace(T, E, device) -> int:
 def _forward(logits, k, balance, z, score, mask, idx, stream) -> RouterLoss:
     lib = load_library()
     T, E = logits.shape
-    with op_stream(logits, stream) as st:
+    with op_stream(logits, stream, logits, mask, idx) as st:
         n = _workspace(T, E, logits.get_device())
         words = 4 + 2 * E + 1
         # one buffer: the result, then the workspace
@@ -149,7 +155,7 @@ def _forward(logits, k, balance, z, score, mask, idx, stream) -> RouterLoss:
         check_op(lib.l4moe_router_loss(
             T, E, k, logits.data_ptr(), ELEMS[logits.dtype], _stride(logits), None if mask is None else mask.data_ptr(),
             None if idx is None else idx.data_ptr(), SCORES[score], balance, z, at, at + 4 * words, n, st))
-    return RouterLoss(logits, mask, SCORES[score], buf)
+    return RouterLoss(logits, mask, SCORES[score], buf, st)
 
 
 class _Loss(torch.autograd.Function):
@@ -160,14 +166,15 @@ class _Loss(torch.autograd.Function):
         r = _forward(logits.detach(), *args)
         box.append(r)
         ctx.save_for_backward(logits, r._result, mask)
-        ctx.score = r._score
+        ctx.score, ctx.home = r._score, r._home
         return r.loss.clone()
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, upstream):
         logits, result, mask = ctx.saved_tensors
-        return RouterLoss(logits.detach(), mask, ctx.score, result).grad(upstream.contiguous()), None, None, None
+        r = RouterLoss(logits.detach(), mask, ctx.score, result, ctx.home)
+        return r.grad(upstream.contiguous()), None, None, None
 
 
 def router_loss(logits: torch.Tensor, k: int = 1, *, balance: float = 1e-2, z: float = 1e-3, score: str = "softmax",

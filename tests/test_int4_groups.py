@@ -298,6 +298,23 @@ def test_streams_capture_and_repeats():
 
 
 @pytest.mark.gpu
+def test_inputs_released_while_another_stream_still_uses_them():
+    x, w, s = make(5, 4096, 2048, 128, "bf16", "f16")
+    want = int4_matvec(x, w, s, 128)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        mine = x.clone()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # about 10 ms: the call below waits behind it
+        y = int4_matvec(mine, w, s, 128, stream=stream)
+        del mine
+        held = [torch.full_like(x, float("nan")) for _ in range(4)]  # would be given mine's memory
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and len(held) == 4
+
+
+@pytest.mark.gpu
 def test_weights_past_two_gigabytes():
     """Byte offsets past 2^31 (rows of 40000 columns, 110000 of them)."""
     K, N, group = 110000, 40000, 128

@@ -445,6 +445,35 @@ def test_a_mask_changed_after_the_call_is_noticed_by_autograd():
 
 
 @pytest.mark.gpu
+def test_tensors_released_while_another_stream_still_uses_them():
+    x = make(4000, 64, "bf16")
+    first = router_loss(x, 2)
+    want, grad = first.loss.clone(), first.grad()
+    side = torch.cuda.Stream()
+    mine = x.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms: the calls below wait behind it
+    r = router_loss(mine, 2, stream=side)
+    del mine
+    r._logits = x  # (the result holds its logits)
+    held = [torch.full_like(x, float("nan")) for _ in range(4)]  # would be given mine's memory
+    torch.cuda.synchronize()
+    assert torch.equal(r.loss, want) and len(held) == 4
+    # the result's own memory, read by a gradient on another stream
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    r = router_loss(x, 2)
+    side.wait_stream(torch.cuda.current_stream())
+    words = r._result.numel()
+    g = r.grad(stream=side)
+    del r
+    held = [torch.full((words,), float("nan"), device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(g, grad) and len(held) == 4
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [700, 40000])
 def test_one_expert_and_padded_batches(T):
     """E = 1, and a batch whose second half is padding (any size of launch)."""
