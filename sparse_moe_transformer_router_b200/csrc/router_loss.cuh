@@ -25,9 +25,9 @@
 // log2 L shuffles and small rows share a warp.  Sums are fp32, always in the
 // same order.
 //
-// For long rows the arithmetic bounds both: 366 warp instructions per row
-// of 256 in the values' pass (counted by a profiler for sigmoid and four
-// choices: exponentials, reciprocals, keys and choices), where HBM delivers the
+// For long rows the arithmetic bounds both: 400 warp instructions per row
+// of 256 in the values' pass and 240 in the gradient's (counted by a profiler
+// for sigmoid and four choices: exponentials, reciprocals, keys and choices), where HBM delivers the
 // 512 bytes in about 90 cycles of a scheduler.  Measured on one B200 (device time of values and
 // gradient together): 65536 x 256 bf16, sigmoid, four choices: 59 to
 // 60 us; 16384 x 128 fp32 18 us; 4096 x 16 bf16 7 us and 64 x 4 fp32
