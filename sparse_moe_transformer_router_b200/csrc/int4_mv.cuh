@@ -353,6 +353,39 @@ __host__ __device__ __forceinline__ int slice_row(int K, int r, int lg) {
     return k < K ? k : K;
 }
 
+// Rows [r0, r1) of part `part` of PARTS of the slice [k0, k1): whole blocks (of
+// the last one what K leaves); the number of blocks.
+__host__ __device__ __forceinline__ int part_rows(int k0, int k1, int part, int PARTS, int& r0, int& r1) {
+    const int nblk = (k1 - k0 + kBlock - 1) / kBlock;
+    const int b0 = nblk * part / PARTS, blocks = nblk * (part + 1) / PARTS - b0;
+    r0 = k0 + b0 * kBlock;
+    r1 = k1 < r0 + blocks * kBlock ? k1 : r0 + blocks * kBlock;
+    return blocks;
+}
+
+// The scales that come with a warp's stages, from row r0 (a multiple of kBlock)
+// on: a half of a stage brings the scales of the group that begins there (the
+// warp's first half always does).
+struct ScaleRows {
+    int group, grp, left, next;  // the latest group; its rows that are left; the next one's rows
+    __host__ __device__ __forceinline__ ScaleRows(int r0, int group_) : group(group_) {
+        grp = r0 / group;
+        left = 0, next = group - (r0 - grp * group);
+        --grp;
+    }
+    // The next stage, at `row` of rows that end at r1: whether its halves bring
+    // scales; those are the rows first(s1) and grp of the scales.
+    __host__ __device__ __forceinline__ void stage(int row, int r1, bool& s0, bool& s1) {
+        s0 = left == 0;
+        if (s0) left = next, next = group, ++grp;
+        left -= kBlock;
+        s1 = left == 0 && row + kBlock < r1;  // (the last stage's second half may have no rows, and no group)
+        if (s1) left = group, ++grp;
+        left -= kBlock;
+    }
+    __host__ __device__ __forceinline__ int first(bool s1) const { return grp - (s1 ? 1 : 0); }
+};
+
 // This warp's sums over part `part` of PARTS of the slice [k0, k1) of K, for
 // the 128 columns from col0 on and nt tokens, left in red [warp][token][128]
 // (over the rings: all warps are through with theirs).  tokens(): the token
@@ -366,38 +399,29 @@ __device__ __forceinline__ bool warp_sums(uint8_t* ring, uint64_t* bar, float* r
     constexpr bool BF = !std::is_same<XT, __half>::value;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const int nblk = (k1 - k0 + kBlock - 1) / kBlock;
-    const int b0 = nblk * part / PARTS, blocks = nblk * (part + 1) / PARTS - b0;
-    const int r0 = k0 + b0 * kBlock, r1 = min(k1, r0 + blocks * kBlock);
+    int r0, r1;
+    const int blocks = part_rows(k0, k1, part, PARTS, r0, r1);
     const int stages = (blocks + 1) >> 1;
     const uint32_t ring0 = op::smem_u32(ring), bar0 = op::smem_u32(bar);
 
-    // ---- loads: the next stage's row, its group and the rows until the group's end
-    int lrow = r0, grp = r0 / W.group, lleft = 0, lnext = W.group - (r0 - grp * W.group);
-    --grp;
-    auto scales_due = [&](bool& s0, bool& s1) {  // which halves of the stage begin a group (the warp's first does)
-        s0 = lleft == 0;
-        if (s0) lleft = lnext, lnext = W.group, ++grp;
-        lleft -= kBlock;
-        s1 = lleft == 0;
-        if (s1) lleft = W.group, ++grp;
-        lleft -= kBlock;
-    };
+    // ---- loads: the next stage's row and the scales that come with it
+    int lrow = r0;
+    ScaleRows scales(r0, W.group);
     int xrow = 0;  // this lane's token's row (lanes below nt)
     Tokens<XT> X{};
     auto issue_w = [&](int s, uint32_t at) {  // the weight's and the scales' part of stage s
         bool s0, s1;
-        scales_due(s0, s1);
+        scales.stage(lrow, r1, s0, s1);
         if constexpr (TMA) {
             if (lane == 0) {
                 const uint32_t b = bar0 + s * 8;
                 op::mbar_expect(b, kRows * 64 + nt * kXRow + ((s0 ? 1 : 0) + (s1 ? 1 : 0)) * kCols * (int)sizeof(ST));
                 op::tma_2d(at, W.qm, b, col0 >> 1, lrow);
-                if (s0) op::tma_2d(at + Cf::SOFF, W.sm, b, col0, grp - (s1 ? 1 : 0));
-                if (s1) op::tma_2d(at + Cf::SOFF + kCols * (int)sizeof(ST), W.sm, b, col0, grp);
+                if (s0) op::tma_2d(at + Cf::SOFF, W.sm, b, col0, scales.first(s1));
+                if (s1) op::tma_2d(at + Cf::SOFF + kCols * (int)sizeof(ST), W.sm, b, col0, scales.grp);
             }
         } else {
-            load_plain<NT8, XT, ST>(ring + (at - ring0), W, col0, X, nt, lrow, r1, s0, s1, grp - (s1 ? 1 : 0), lane);
+            load_plain<NT8, XT, ST>(ring + (at - ring0), W, col0, X, nt, lrow, r1, s0, s1, scales.first(s1), lane);
         }
     };
     auto issue_x = [&](int s, uint32_t at) {
@@ -444,7 +468,6 @@ __device__ __forceinline__ bool warp_sums(uint8_t* ring, uint64_t* bar, float* r
     int left = 0, next = W.group - r0 % W.group;  // rows that the scales at hand still cover; of the next ones
     bool ok = true;
     uint32_t parity = 0;
-    int todo = stages - pre;  // stages still to load
     for (int i0 = 0; i0 < stages && ok; i0 += Cf::STAGES, parity ^= 1u) {
 #pragma unroll
         for (int s = 0; s < Cf::STAGES; ++s) {
@@ -474,8 +497,7 @@ __device__ __forceinline__ bool warp_sums(uint8_t* ring, uint64_t* bar, float* r
                 block_fma<NT8, BF>(acc, rows0 + s * Cf::STAGE + h * kBlock * 64,
                                    (x0 + s * Cf::STAGE) ^ (h * 64), sc, f);
             }
-            if (todo > 0) {
-                --todo;
+            if (lrow < r1) {  // a stage still to load
                 __syncwarp();  // every lane has read the stage
                 issue_w(s, ring0 + s * Cf::STAGE);
                 issue_x(s, ring0 + s * Cf::STAGE);

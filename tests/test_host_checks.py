@@ -7,6 +7,8 @@
 - the grouped GEMM's tile schedule (tile_at, decode_tile) on random work
   lists: every tile decoded exactly once and inside its group
   (tests/host/schedule_check.cu);
+- the scale rows that the int4 products' warps ask for, over sizes, groups,
+  slices and warps (tests/host/int4_scales_check.cu);
 - the workspace layout and split-K plan of the library's host code on random
   shapes, dtypes, k and token budgets: aligned, ordered segments large
   enough for any smaller batch, partial planes included
@@ -46,3 +48,8 @@ def test_gemm_tile_schedule_covers_every_tile_once(tmp_path):
 @pytest.mark.skipif(NVCC is None, reason="nvcc not available")
 def test_workspace_layout_holds_every_smaller_batch(tmp_path):
     _build_and_run("layout_check.cu", tmp_path / "layout_check", extra=("-O1",))
+
+
+@pytest.mark.skipif(NVCC is None, reason="nvcc not available")
+def test_int4_products_read_scale_rows_that_exist(tmp_path):
+    _build_and_run("int4_scales_check.cu", tmp_path / "int4_scales_check")
