@@ -21,7 +21,10 @@ with dropped entries (any index outside [0, E)).
 
 Where the logits take part in autograd (a leaf or the output of the router's
 product), `r.loss` has their gradient: `(task_loss + r.loss).backward()`.
-The other values carry none.  Before a backward pass is captured into a CUDA
+The other values carry none.  With `stream`, everything the call computes is
+that stream's work: wait for it before using the values on another one.  The
+backward pass of `r.loss` runs there too, and autograd makes the streams wait
+for one another around it.  Before a backward pass is captured into a CUDA
 graph, let go of eager losses of the same leaves, as for any torch function.
 One pass reads the logits for the values, one
 more for the gradient; everything runs in the library's CUDA kernels on the
@@ -143,7 +146,7 @@ def _workspace(T, E, device) -> int:
     return load_library().l4moe_router_loss_workspace(T, E)
 
 
-def _forward(logits, k, balance, z, score, mask, idx, stream) -> RouterLoss:
+def _forward(logits, k, balance, z, score, mask, idx, stream=None) -> RouterLoss:
     lib = load_library()
     T, E = logits.shape
     with op_stream(logits, stream, logits, mask, idx) as st:
@@ -189,11 +192,12 @@ def router_loss(logits: torch.Tensor, k: int = 1, *, balance: float = 1e-2, z: f
     k = int(k)
     if not _accepts(logits, k, score, mask, idx):
         _refuse(logits, k, score, mask, idx)
-    args = (k, float(balance), float(z), score, mask, idx, stream)
+    args = (k, float(balance), float(z), score, mask, idx)
     if not (logits.requires_grad and torch.is_grad_enabled()):
-        return _forward(logits, *args)
+        return _forward(logits, *args, stream)
     box = []
-    loss = _Loss.apply(logits, mask, args, box)
+    with op_stream(logits, stream, logits, mask, idx):  # the loss's copy and its backward pass are that stream's too
+        loss = _Loss.apply(logits, mask, args, box)
     r = box[0]
     r.loss = loss
     return r

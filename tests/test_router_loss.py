@@ -137,6 +137,48 @@ def test_a_gradient_over_its_logits_is_refused():
             assert grad(**kw) == binding.ERR_CUDA, kw
 
 
+def test_the_loss_of_another_stream_is_copied_on_that_stream(monkeypatch):
+    """Without a GPU: stand-ins for the stream scope and the library note where
+    the values, the loss's copy for autograd and its gradient are enqueued."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    from sparse_moe_transformer_router_b200 import router_loss as module
+    current, seen = ["own"], []
+
+    class Scope:
+        def __init__(self, tensor, stream, *used):
+            self.stream = current[-1] if stream is None else stream
+
+        def __enter__(self):
+            current.append(self.stream)
+            return self.stream
+
+        def __exit__(self, *exc):
+            current.pop()
+
+    class Library:
+        def l4moe_router_loss(self, *args):
+            seen.append(("values", args[-1]))
+            return 0
+
+    class Copies(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            if func.overloadpacket is torch.ops.aten.clone:
+                seen.append(("copy", current[-1]))
+            return func(*args, **(kwargs or {}))
+
+    monkeypatch.setattr(module, "op_stream", Scope)
+    monkeypatch.setattr(module, "load_library", Library)
+    monkeypatch.setattr(module, "_accepts", lambda *args: True)
+    monkeypatch.setattr(module, "_workspace", lambda *args: 0)
+    for stream in ("side", None):
+        seen.clear()
+        with Copies():
+            r = module.router_loss(torch.zeros(4, 8).requires_grad_(), 1, stream=stream)
+        where = stream or "own"
+        assert r.loss.requires_grad and seen == [("values", where), ("copy", where)]
+
+
 def test_refusals_of_the_library():
     lib = binding.load_library()
     A = 256  # a pointer value that no refused call follows
@@ -388,6 +430,33 @@ def test_streams_and_two_calls_at_once():
     for r1, g1, r2, g2 in got:
         assert torch.equal(r1.loss, want[0][0]) and torch.equal(g1, want[0][1])
         assert torch.equal(r2.loss, want[1][0]) and torch.equal(g2, want[1][1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("raw", [False, True])
+def test_autograd_of_a_call_on_another_stream(raw):
+    """The loss and its gradient, with a side stream that is busy when the
+    values are asked for and again before the backward pass."""
+    x, own = make(3000, 24, "f32", seed=4), torch.cuda.current_stream()
+    ref = reference(x, 2, 0.5, 0.25)
+    side = torch.cuda.Stream()
+    for busy in range(2):
+        leaf = x.clone().requires_grad_()
+        side.wait_stream(own)
+        with torch.cuda.stream(side):
+            # (the memory that the result will be given, with other values)
+            other = router_loss(torch.zeros_like(x), 2)
+            del other
+            torch.cuda._sleep(20_000_000)  # about 10 ms
+        r = router_loss(leaf * 1.0 if busy else leaf, 2, balance=0.5, z=0.25,
+                        stream=side.cuda_stream if raw else side)
+        own.wait_stream(side)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        (3.0 * r.loss).backward()
+        g = leaf.grad.clone()
+        torch.cuda.synchronize()
+        check(r, ref, x, 0.5, 0.25, up=3.0, grad=g)
 
 
 @pytest.mark.gpu
