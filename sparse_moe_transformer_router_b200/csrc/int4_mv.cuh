@@ -386,6 +386,18 @@ struct ScaleRows {
     __host__ __device__ __forceinline__ int first(bool s1) const { return grp - (s1 ? 1 : 0); }
 };
 
+// Stage i of a warp is load i of its ring: slot i % STAGES, the barrier's phase
+// of this parity.
+template <int STAGES>
+__host__ __device__ __forceinline__ uint32_t stage_parity(int i) { return (uint32_t)(i / STAGES) & 1u; }
+
+// After the wait for stage `at` of `stages` gave up: wait(slot, parity) for
+// every copy that is on its way.
+template <int STAGES, typename W>
+__host__ __device__ __forceinline__ void drain(int at, int stages, W&& wait) {
+    for (int i = at; i < at + STAGES && i < stages; ++i) wait(i % STAGES, stage_parity<STAGES>(i));
+}
+
 // This warp's sums over part `part` of PARTS of the slice [k0, k1) of K, for
 // the 128 columns from col0 on and nt tokens, left in red [warp][token][128]
 // (over the rings: all warps are through with theirs).  tokens(): the token
@@ -467,14 +479,17 @@ __device__ __forceinline__ bool warp_sums(uint8_t* ring, uint64_t* bar, float* r
     float sc[16];
     int left = 0, next = W.group - r0 % W.group;  // rows that the scales at hand still cover; of the next ones
     bool ok = true;
-    uint32_t parity = 0;
-    for (int i0 = 0; i0 < stages && ok; i0 += Cf::STAGES, parity ^= 1u) {
+    for (int i0 = 0; i0 < stages && ok; i0 += Cf::STAGES) {
 #pragma unroll
         for (int s = 0; s < Cf::STAGES; ++s) {
             if (i0 + s >= stages) break;
             if constexpr (TMA) {
-                ok = __all_sync(0xffffffffu, op::mbar_wait(bar0 + s * 8, parity));
-                if (!ok) break;
+                ok = __all_sync(0xffffffffu, op::mbar_wait(bar0 + s * 8, stage_parity<Cf::STAGES>(i0)));
+                if (!ok) {  // let what is on its way arrive before the memory is used again
+                    drain<Cf::STAGES>(i0 + s, stages,
+                                      [&](int slot, uint32_t parity) { op::mbar_wait(bar0 + slot * 8, parity); });
+                    break;
+                }
             } else {
                 __syncwarp();
             }
@@ -503,9 +518,6 @@ __device__ __forceinline__ bool warp_sums(uint8_t* ring, uint64_t* bar, float* r
                 issue_x(s, ring0 + s * Cf::STAGE);
             }
         }
-    }
-    if (TMA && !ok) {  // let what is on its way arrive before the memory is used again
-        for (int s = 0; s < Cf::STAGES; ++s) op::mbar_wait(bar0 + s * 8, parity);
     }
     const float bad = ok ? 0.f : __int_as_float(0x7fffffff);
     __syncthreads();

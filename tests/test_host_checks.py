@@ -9,6 +9,8 @@
   (tests/host/schedule_check.cu);
 - the scale rows that the int4 products' warps ask for, over sizes, groups,
   slices and warps (tests/host/int4_scales_check.cu);
+- the waits for a warp's copies in flight once one did not come in time
+  (tests/host/int4_ring_check.cu);
 - the workspace layout and split-K plan of the library's host code on random
   shapes, dtypes, k and token budgets: aligned, ordered segments large
   enough for any smaller batch, partial planes included
@@ -53,3 +55,8 @@ def test_workspace_layout_holds_every_smaller_batch(tmp_path):
 @pytest.mark.skipif(NVCC is None, reason="nvcc not available")
 def test_int4_products_read_scale_rows_that_exist(tmp_path):
     _build_and_run("int4_scales_check.cu", tmp_path / "int4_scales_check")
+
+
+@pytest.mark.skipif(NVCC is None, reason="nvcc not available")
+def test_int4_products_wait_for_their_copies_after_a_timeout(tmp_path):
+    _build_and_run("int4_ring_check.cu", tmp_path / "int4_ring_check")
