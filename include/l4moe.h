@@ -198,7 +198,9 @@ L4MOE_API l4moe_status l4moe_set_fp8_scales(l4moe_handle *h, const float *const 
  * f16 (L4MOE_ERR_RANGE past it), fp32 sums; no weight is rounded.  Its
  * products then run for up to 8 rows of an expert at a time (built for the
  * small batches of decode; longer batches read an expert's weights again for
- * every 8 rows). */
+ * every 8 rows).  A forward of T tokens and k experts per token is refused
+ * (L4MOE_ERR_ARG) where min(T k, E + T k / 8) + T / 8, the tiles of 8 rows, may
+ * pass 65535: some 260 thousand tokens at k = 1, 104 thousand at k = 4. */
 L4MOE_API l4moe_status l4moe_set_group_scales(l4moe_handle *h, int group, l4moe_elem type, const void *const *s_gate_up,
                                     const void *const *s_down, const void *ss_gate_up, const void *ss_down);
 

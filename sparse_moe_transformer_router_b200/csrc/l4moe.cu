@@ -334,6 +334,17 @@ bool encode_group_maps(l4moe_handle* h, const void* const* Wgu, const void* cons
     return true;
 }
 
+// Tiles of 8 rows of one expert that T k entries make at most (every one holds
+// an entry), and the units of a launch of experts with group scales: those and
+// the shared expert's, at most kMaxUnits (the grid's y axis).
+constexpr long long kMaxUnits = 65535;
+long long routed_tiles(int E, long long entries) {
+    return E > 0 ? std::min(entries, std::min<long long>(E, entries) + entries / 8) : 0;
+}
+long long group_units(const l4moe_handle* h, int T) {
+    return routed_tiles(h->p.num_experts, (long long)T * h->top_k) + ((long long)T + 7) / 8;
+}
+
 // Encode the weight descriptors on the host (h->h_maps) unless they already
 // describe these pointers.
 l4moe_status encode_weight_maps(l4moe_handle* h, const void* const* Wgu, const void* const* Wdn,
@@ -610,8 +621,7 @@ l4moe_status run_layer(l4moe_handle* h, int T, const void* x, const void* Wr, co
     // experts with group scales, a few tokens: routing without row copies
     // (the products gather their bf16 rows themselves)
     const bool gather = grouped && E > 0 && T <= rg::kTokens && E % 8 == 0;
-    // tiles of 8 rows of one expert: every one holds an entry
-    const int routed_units = E > 0 ? std::min(Tv, std::min(E, Tv) + Tv / 8) : 0;
+    const int routed_units = (int)routed_tiles(E, Tv);
     if (gather) {
         static std::atomic<uint64_t> attr_done{0};
         ensure_smem_attr(attr_done, rg::route_group_kernel, rg::smem_bytes());
@@ -751,8 +761,7 @@ l4moe_status run_layer(l4moe_handle* h, int T, const void* x, const void* Wr, co
                 return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, (uint64_t)width, (uint64_t)n,
                                  2 * (uint64_t)width, mv::kRows, 1);
             };
-            const int units = routed_units + (T + 7) / 8, per_sm = mv::Cfg<1, float>::PER_SM;
-            if (units > 65535) return fail(h, L4MOE_ERR_ARG, "batch too long for experts with group scales");
+            const int units = (int)group_units(h, T), per_sm = mv::Cfg<1, float>::PER_SM;
             // without experts the routed operand is never read
             if (!rows_map(&R.xm[0], gather || !has ? x16 : xg, d, gather || !has ? T : Tv) ||
                 !rows_map(&R.xm[1], x16, d, T))
@@ -995,6 +1004,8 @@ l4moe_status check_forward_args(l4moe_handle* h, int T, const void* x, const voi
     }
     if (coded8(h->p.dtype) && !h->ss_gu)
         return fail(h, L4MOE_ERR_DTYPE, "8-bit weights need l4moe_set_weight_scales first");
+    if (h->group && group_units(h, T) > kMaxUnits)
+        return fail(h, L4MOE_ERR_ARG, "batch too long for experts with group scales");
     return L4MOE_OK;
 }
 

@@ -637,3 +637,25 @@ def test_layer_refusals():
     other = L4MoE(64, 64, 64, 2, "int8")
     assert lib.l4moe_set_group_scales(other._h, 32, 0, arr, arr, 256, 256) == binding.ERR_DTYPE
     m.run_and_check(m.tokens(3))  # the refused calls changed nothing
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,k,T", [(4, 2, 174_800), (0, 1, 524_289)])
+def test_a_batch_past_the_units_of_a_launch_is_refused_before_anything_runs(E, k, T):
+    """The grid's y axis holds 65535 units of up to 8 rows: at most min(E, T k)
+    + T k / 8 of routed rows and T / 8 of the shared expert's."""
+    m = Layer(64, 64 if E else 0, 64, E, 32, "f16", k)
+    few = m.tokens(5)
+    want = m.run_and_check(few)
+    routed = {n: v.clone() for n, v in m.layer.routing().items()} if E else {}
+    launches = m.layer.launch_count
+    x = torch.zeros(T, 64, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(x, 7.0)
+    with pytest.raises(L4MoEError, match="batch too long") as err:
+        m.layer.forward(x, *m.weights(), out=out)
+    assert err.value.status == binding.ERR_ARG
+    assert m.layer.launch_count == launches and bool((out == 7.0).all())
+    if E:
+        assert all(torch.equal(v, routed[n]) for n, v in m.layer.routing().items())
+    m.layer.check_device_status()
+    assert torch.equal(m.layer.forward(few, *m.weights()), want)
