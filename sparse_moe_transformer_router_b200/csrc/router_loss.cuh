@@ -164,10 +164,12 @@ template <typename IT, int L, bool SIG>
 struct RowStats {
     float ex[kLossPer], sg[kLossPer], q[kLossPer], inv, iw, lse;
 
-    // The usual rows: the sum of e^l is neither tiny nor near fp32's end in
-    // any of the warp's rows, so nothing need be subtracted first, and
-    // sigma(l) = e^l / (1 + e^l) takes no exponential of its own.  False, for
-    // the whole warp: not usual (a NaN, +inf, nothing above -inf, ...).
+    // The usual rows: the sum of e^l is in (1e-12, 1e20) in all of the warp's
+    // rows, so nothing need be subtracted first, and sigma(l) = e^l / (1 +
+    // e^l) takes no exponential of its own.  The bounds leave fp32's range to
+    // what the gradient multiplies with: its factors (those of 2^31 rows are
+    // near 1e-10, a loss scale of f16 is 65536) times the sum or 1 / the sum.
+    // False, for the whole warp: not usual (a NaN, +inf, nothing above -inf, ...).
     __device__ __forceinline__ bool usual(const float (&v)[kLossPer]) {
         float s = 0.f;
 #pragma unroll
@@ -176,7 +178,7 @@ struct RowStats {
             s += ex[i];
         }
         s = row_sum<L>(s);
-        if (__any_sync(0xffffffffu, !(s > 1e-12f && s < 1e37f))) return false;
+        if (__any_sync(0xffffffffu, !(s > 1e-12f && s < 1e20f))) return false;
         inv = hw_rcp(s);
         lse = hw_log2(s) * 0.693147181f;
         if constexpr (SIG) {

@@ -374,6 +374,23 @@ def test_sigmoid_scores_of_very_low_and_very_high_logits():
               reference(logits, 2, 1.0, 0.0, "sigmoid"), logits, 1.0, 0.0)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T,up", [(2, 65536.0), (3000, 1.0)])
+def test_rows_of_large_and_small_logits(T, up, dtype, score):
+    """exp of these is far from 1 and still inside fp32's range; a gradient's
+    factors times its reciprocal, or its sums, need not be."""
+    base = torch.randn(T, 16, generator=torch.Generator().manual_seed(5))
+    for shift in (-60.0, -26.0, 30.0, 45.0, 60.0, 80.0):
+        logits = (base + shift).to(TYPES[dtype]).cuda()
+        # (the long batch's choices, the same ones, are given: the reference's own take long)
+        idx = None if T == 2 else torch.sort(logits, dim=1, descending=True, stable=True).indices[:, :2].int().contiguous()
+        for wb, wz in ((1e-2, 0.0), (0.5, 1e-3)):
+            check(router_loss(logits, 2, balance=wb, z=wz, score=score, idx=idx),
+                  reference(logits, 2, wb, wz, score, idx=idx), logits, wb, wz, up=up)
+
+
 # --------------------------------------------------------------------- the calls
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(TYPES))
