@@ -61,39 +61,63 @@ def _includes(path: str, seen=None) -> set:
     return seen
 
 
+def _made_by(nvcc: str, flags) -> str:
+    """What an object is made by besides its sources: the compiler and the flags."""
+    version = subprocess.run([nvcc, "--version"], capture_output=True, text=True, check=True).stdout
+    return "\n".join([os.path.realpath(nvcc), version, *flags])
+
+
+def _kept(src: str, obj: str, stamp: str, made_by: str) -> bool:
+    """Whether obj is newer than all it includes and was made by the same compiler and flags."""
+    if not (os.path.exists(obj) and os.path.exists(stamp)):
+        return False
+    with open(stamp) as f:
+        if f.read() != made_by:
+            return False
+    return all(os.path.getmtime(p) <= os.path.getmtime(obj) for p in _includes(src))
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every source (side by side; one whose object is newer than all
-    it includes is kept) and link the library."""
+    it includes, and made by the same compiler and flags, is kept) and link the
+    library."""
     if not force and up_to_date():
         return LIB
     os.makedirs(OBJ, exist_ok=True)
     flags = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
              "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC]
+    nvcc = _nvcc()
+    made_by = _made_by(nvcc, flags)
     if verbose:
         flags.insert(0, "-Xptxas=-v")
     jobs, objects = [], []
     for src in _sources():
         obj = os.path.join(OBJ, os.path.basename(src)[:-3] + ".o")
         objects.append(obj)
-        if not force and os.path.exists(obj) and \
-                all(os.path.getmtime(p) <= os.path.getmtime(obj) for p in _includes(src)):
+        stamp = obj + ".made_by"
+        if not force and _kept(src, obj, stamp, made_by):
             continue
         tmp = f"{obj}.tmp{os.getpid()}.o"
-        cmd = [_nvcc(), *flags, "-c", src, "-o", tmp]
-        jobs.append((cmd, tmp, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+        cmd = [nvcc, *flags, "-c", src, "-o", tmp]
+        jobs.append((cmd, tmp, obj, stamp,
+                     subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
     failed = None
-    for cmd, tmp, obj, p in jobs:
+    for cmd, tmp, obj, stamp, p in jobs:
         out = p.communicate()[0]
         if verbose or p.returncode != 0:
             sys.stderr.write(out)
         if p.returncode != 0:
             failed = f"nvcc failed ({p.returncode}): {' '.join(cmd)}"
         else:
+            if os.path.exists(stamp):  # (an object never stands beside another's stamp)
+                os.remove(stamp)
             os.replace(tmp, obj)
+            with open(stamp, "w") as f:
+                f.write(made_by)
     if failed:
         raise RuntimeError(failed)
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objects]
+    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objects]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
