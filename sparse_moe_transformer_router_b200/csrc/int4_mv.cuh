@@ -77,6 +77,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kCols = 128;       // columns of a warp
 constexpr int kBlock = 32;       // rows that share a scale at least (scale groups are multiples of it)
 constexpr int kRows = 64;        // rows of a stage
+constexpr int kStages = 2;       // of a warp's ring
 constexpr int kXRow = 2 * kRows; // bytes of a token's row in a stage
 
 // A warp's ring.  Stage: the weight's 64 rows of 64 bytes, the tokens' 64
@@ -90,7 +91,7 @@ struct Cfg {
     // thread, 16 tokens 168).  Four with two stages each beat three with
     // three (1 x 5120 x 202048: 111 against 118 us): the arithmetic wants the warps
     static constexpr int PER_SM = NT8 == 1 ? 4 : 3;
-    static constexpr int STAGES = 2;
+    static constexpr int STAGES = kStages;
     static constexpr int RING = STAGES * STAGE;
     static constexpr int RED = (int)sizeof(float) * kWarps * NT8 * 8 * kCols;  // over the rings
     static constexpr int SMEM = (kWarps * RING > RED ? kWarps * RING : RED) + 1024;  // and room to align them
@@ -497,7 +498,6 @@ __device__ __forceinline__ bool warp_sums(uint8_t* ring, uint64_t* bar, float* r
             for (int h = 0; h < 2; ++h) {
                 if (2 * (i0 + s) + h >= blocks) break;
                 if (left == 0) {  // a group's first rows bring its scales
-                    
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         ST v[4];
@@ -565,7 +565,7 @@ __device__ __forceinline__ float cluster_total(const float* red, int i, int slic
 
 // This warp's ring and barriers in a kernel's shared memory; all threads.
 template <int NT8, typename ST>
-__device__ __forceinline__ uint8_t* rings(uint8_t* smem, uint64_t (&bar)[kWarps][3]) {
+__device__ __forceinline__ uint8_t* rings(uint8_t* smem, uint64_t (&bar)[kWarps][kStages]) {
     using Cf = Cfg<NT8, ST>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (lane == 0) {
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT8, ST>::PER_SM) int4_matvec_ke
     const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap sm,
     const __grid_constant__ CUtensorMap xm, const XT* __restrict__ x, int T, Weight<ST> W, XT* __restrict__ y) {
     extern __shared__ __align__(16) uint8_t mv_smem[];
-    __shared__ uint64_t bar[kWarps][3];
+    __shared__ uint64_t bar[kWarps][kStages];
     uint8_t* base = rings<NT8, ST>(mv_smem, bar);
     op::pdl_enter();
     const int warp = threadIdx.x >> 5;
@@ -680,7 +680,7 @@ __device__ __forceinline__ int2 find_unit(const GroupTable* tab, int u) {
 template <typename ST, bool GATE_UP>
 __global__ void __launch_bounds__(kThreads, Cfg<1, ST>::PER_SM) experts_kernel(const __grid_constant__ Rows R) {
     extern __shared__ __align__(16) uint8_t mv_smem[];
-    __shared__ uint64_t bar[kWarps][3];
+    __shared__ uint64_t bar[kWarps][kStages];
     uint8_t* base = rings<1, ST>(mv_smem, bar);
     const int warp = threadIdx.x >> 5;
     // the shared expert's units come first: their weights are on their way

@@ -618,8 +618,8 @@ l4moe_status run_layer(l4moe_handle* h, int T, const void* x, const void* Wr, co
     // split-K k-ranges when a small batch leaves too few tiles
     const SplitPlan plan = split_plan(p, T, h->sms, h->top_k, ACT8);
     const int s_gu = plan.s_gu, s_dn = plan.s_dn;
-    // experts with group scales, a few tokens: routing without row copies
-    // (the products gather their bf16 rows themselves)
+    // experts with group scales, a few tokens: routing without row copies (the
+    // products gather their rows themselves, from the f16 ones that it writes)
     const bool gather = grouped && E > 0 && T <= rg::kTokens && E % 8 == 0;
     const int routed_units = (int)routed_tiles(E, Tv);
     if (gather) {

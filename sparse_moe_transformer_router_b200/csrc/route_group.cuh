@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) route_group_kernel(
                 const __nv_bfloat16* src = Wr + (size_t)next * kStep * E + c0;
                 for (int i = lane; i < kStep * chunks; i += 32) {
                     const int r = i / chunks, c = i - r * chunks;
-                    op::cp_async<16>(ring0 + stage * kStage + r * kPitch + c * 16, src + (size_t)r * E + c * 8);
+                    op::cp_async16(ring0 + stage * kStage + r * kPitch + c * 16, src + (size_t)r * E + c * 8);
                 }
             }
             next += stride;

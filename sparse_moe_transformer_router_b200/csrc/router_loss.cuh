@@ -287,7 +287,7 @@ __device__ __forceinline__ void order(uint32_t& a, uint32_t& b) {
 // is counted), `key` holding a 32-bit key per expert whose low 10 bits are
 // 1023 - expert: the largest key is the next choice.
 template <int L>
-__device__ __forceinline__ void count_keys(uint32_t (&key)[kLossPer], int k, int E, bool adds, int* counts) {
+__device__ __forceinline__ void count_keys(uint32_t (&key)[kLossPer], int k, bool adds, int* counts) {
     if (k <= 2) {
         uint32_t best = key[0];
 #pragma unroll
@@ -368,7 +368,7 @@ __device__ __forceinline__ void count_choices16(const Raw<IT>& raw, const float 
         for (int i = 0; i < kLossPer; ++i)
             key[i] = e0 + i < E ? (choice_key(v[i]) & ~1023u) | (uint32_t)(1023 - (e0 + i)) : 0u;
     }
-    count_keys<L>(key, k, E, adds, counts);
+    count_keys<L>(key, k, adds, counts);
 }
 
 // The same of fp32 logits: the largest value, then the lowest index that holds it.
