@@ -76,7 +76,11 @@
  *
  * Requirements: d, F, Fs multiples of 64; 0 <= E <= 256 (F > 0 when E > 0); all tensor pointers
  * 16-byte aligned.  One handle serves one stream at a time (the workspace is
- * shared by the calls made with it).  The library sees raw pointers, not
+ * shared by the calls made with it).  A forward recorded under stream capture
+ * uses the handle's workspace and weight descriptors at every replay: it needs
+ * the handle alive, still keyed to the same weights and scales, and a
+ * workspace that no longer batch has replaced meanwhile (l4moe_set_workspace
+ * for the longest one, or run that one first).  The library sees raw pointers, not
  * buffer sizes: every tensor must hold at least the elements its layout above
  * states, or the kernels read or write past it (the Python binding checks
  * shapes and dtypes before it calls in).
@@ -383,7 +387,8 @@ typedef enum { L4MOE_SCORE_SOFTMAX = 0, L4MOE_SCORE_SIGMOID = 1 } l4moe_score;
  *   loss     = balance_weight balance + z_weight z
  * over the n counted rows: those that mask [T] keeps (bytes, 0 = left out;
  * NULL = all) and that hold a logit other than -inf.  A NaN or +inf in a
- * counted row makes balance, z and loss NaN; rows left out may hold anything.
+ * counted row makes z and loss NaN, and balance too, except that a +inf under
+ * the sigmoid score is a sigmoid of 1 there; rows left out may hold anything.
  * With no counted row all values are 0.  logits [T, E] of `type`, rows ld
  * elements apart, 1 <= E <= 256, 1 <= k <= min(4, E).  idx NULL: each row
  * chooses as the layer's router does (the k largest logits, the lower index
@@ -406,7 +411,7 @@ L4MOE_API l4moe_status l4moe_router_loss(int T, int E, int k, const void *logits
  * device fp32, NULL = 1): dlogits [T, E] of the logits' type, rows ldd
  * elements apart.  logits, type, ld, mask and score as in the call that
  * filled result.  The counts have no derivative.  Rows left out get zeros.
- * dlogits must not overlap the logits. */
+ * dlogits must not overlap the logits or another input. */
 L4MOE_API l4moe_status l4moe_router_loss_grad(int T, int E, const void *logits, l4moe_elem type, long long ld,
                                     const uint8_t *mask, l4moe_score score, const float *result,
                                     const float *upstream, void *dlogits, long long ldd, void *stream);
@@ -424,7 +429,10 @@ L4MOE_API l4moe_status l4moe_router_loss_grad(int T, int E, const void *logits, 
  * is taken exactly; bf16 rows are divided by a power of two into f16's range,
  * exact down to 2^-31 of the row's largest magnitude and to 2^-39 of it
  * below.  A row of x with an infinity or a NaN gives NaN in all its outputs;
- * the other rows are not touched by it.  y must not overlap an input; w need
+ * the other rows are not touched by it.  A copy inside the kernel that does
+ * not come within a second gives NaN in y as well: without a handle there is
+ * no device word that could tell it (a layer's is read by
+ * l4moe_check_device_status).  y must not overlap an input; w need
  * not differ between calls in flight; tensors 16-byte aligned, contiguous, on the current device. */
 #define L4MOE_INT4_MAX_TOKENS 64
 L4MOE_API l4moe_status l4moe_int4_matvec(int T, int K, int N, int group, const void *x, l4moe_elem x_type,

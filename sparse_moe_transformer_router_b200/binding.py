@@ -501,7 +501,10 @@ class L4MoE:
 class BoundLayer:
     """An `L4MoE` with the weights it runs (`L4MoE.bind`).  The tensors are
     held, not copied: values written into them later are used, and moving
-    their storage (`.data = `, `.set_()`) needs a new bind."""
+    their storage (`.data = `, `.set_()`) needs a new bind.  A call captured
+    into a CUDA graph uses the layer's workspace and its weights' descriptors
+    at every replay: run the longest batch (or `set_workspace`) before the
+    capture, and keep the layer, its weights and its scales as they were."""
 
     def __init__(self, layer: L4MoE, W_router, W_gate_up, W_down, Ws_gate_up, Ws_down):
         self.layer = layer

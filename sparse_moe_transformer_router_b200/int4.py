@@ -8,7 +8,9 @@ a multiple of 32:
 
     y[t, n] = sum_k x[t, k] q[k, n] scales[k // group, n]
 
-in fp32, rounded once to x's type.  An inference product: it records no
+in fp32, rounded once to x's type.  NaN stands for what could not be computed:
+a row of x that is not finite, and columns whose copies inside the kernel did
+not come within a second.  An inference product: it records no
 gradient, and refuses an x that asks for one.
 """
 from __future__ import annotations

@@ -14,6 +14,9 @@ sigmoid(logits_te) / sum_j sigmoid(logits_tj) (score="sigmoid"):
     z       = mean_t(logsumexp(logits_t)^2)
     loss    = balance_weight balance + z_weight z
 
+A NaN or +inf in a counted row makes z and loss NaN, and balance too, except
+that a +inf under score="sigmoid" is a sigmoid of 1 there.
+
 Each row chooses its k largest logits as the layer's router does (the lower
 index first among equal ones), or idx [T, k] holds the choices: those of a
 layer that has run (`layer.routing()["idx"]`), of a router with its bias, or

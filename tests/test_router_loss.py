@@ -365,6 +365,21 @@ def test_nan_in_a_counted_row_reaches_the_loss(value):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_an_infinite_logit_is_a_sigmoid_of_one(dtype):
+    """balance keeps a value, z and the loss do not."""
+    logits = make(50, 8, dtype)
+    logits[3, 2] = math.inf
+    r = router_loss(logits, 2, balance=0.5, z=0.25, score="sigmoid")
+    ref = reference(logits, 2, 0.5, 0.25, "sigmoid")
+    assert torch.equal(r.counts.cpu().long(), ref["counts"])
+    assert abs(r.balance.item() - float(ref["balance"])) <= REL * float(ref["balance"])
+    assert math.isnan(r.z.item()) and math.isnan(r.loss.item())
+    g = r.grad()
+    assert bool(torch.isnan(g[3]).any()) and bool(torch.isfinite(g[:3]).all()) and bool(torch.isfinite(g[4:]).all())
+
+
+@pytest.mark.gpu
 def test_sigmoid_scores_of_very_low_and_very_high_logits():
     """Sigmas that underflow in 32 bits (their shares do not), and that are 1."""
     base = torch.randn(40, 12, generator=torch.Generator().manual_seed(0))
