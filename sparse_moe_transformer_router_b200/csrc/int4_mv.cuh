@@ -53,8 +53,13 @@
 // rows x 128 columns a warp needs 80 and 18 of them beside 32 fp32 FMAs.
 // Measured on one B200 (device time, three weights in turn):
 //   1 x 5120 x 202048, groups of 128   110 us   4.8 TB/s   0.74 of the copy rate
+//     (at 1965 MHz; a second of such calls on end, replayed or not, brings the
+//     power cap, 1700 MHz and 125 to 127 us)
 //   1 x 5120 x 16384                    16 us   2.7 TB/s   (1 x 512 x 128 alone takes 3.9 us)
 //   16 x 8192 x 5120, groups of 64      15 us   1.5 TB/s   (two token columns: twice the products)
+//   8 x 5120 x 16384 bf16               21 us   2.0 TB/s
+//   16 x 5120 x 16384 bf16              43 us   1.0 TB/s   (each warp of each column tile finds the rows'
+//     powers of two and converts them again; 256 CTAs for 444 places; some registers spill)
 // The layer's figures stand at experts_kernel.
 #pragma once
 #include <cuda.h>
@@ -462,6 +467,10 @@ __device__ __forceinline__ bool warp_sums(uint8_t* ring, uint64_t* bar, float* r
 
     float factors = 1.f, f[NT8];
     if constexpr (BF) {
+        // up to two loads a lane (512 values) nothing is gained from eight at
+        // once, and the extra steps show: always 2 against always 8, 1 x 512 x
+        // 128 3.86 and 4.03 us, 1 x 8192 x 5120 11.9 and 12.1; above, 8 x 5120
+        // x 16384 22.3 and 20.9, 16 x 5120 x 16384 47.0 and 42.0
         if (blocks > 0)
             factors = nt * (r1 - r0) <= 512 ? find_factors<2>(X, nt, r0, r1, lane) : find_factors<8>(X, nt, r0, r1, lane);
     }
@@ -674,8 +683,8 @@ __device__ __forceinline__ int2 find_unit(const GroupTable* tab, int u) {
 // widens them.  8 rows of an expert at a time; more rows of one expert
 // read its weights again.  Layer of width 5120 and 8192, one B200, device time
 // of a whole forward: one token, 128 experts, groups of 128: 53 us (131 MB,
-// 2.5 TB/s); sixteen tokens, 16 experts, groups of 32: 198 to 201 us (800 MB,
-// 4.0 TB/s).  Between events, which keep the launches from overlapping:
+// 2.5 TB/s); sixteen tokens, 16 experts, groups of 32: 195 to 201 us (800 MB,
+// 4.0 to 4.1 TB/s).  Between events, which keep the launches from overlapping:
 // routing 17, gate/up 29, down 23 us and 15, 127, 72 us.
 template <typename ST, bool GATE_UP>
 __global__ void __launch_bounds__(kThreads, Cfg<1, ST>::PER_SM) experts_kernel(const __grid_constant__ Rows R) {
